@@ -58,10 +58,11 @@ typedef enum xlpk_dtype {
   XLPK_DTYPE_FP8_E4M3 = 1,     /* e4m3 codes, row-major [N][K], + one fp32 scale per 128x128 block;
                                   dense models only, hidden / n_q_heads*head_dim / ffn multiples
                                   of 256 and the other dims of 128 (else XLPK_ERR_UNSUPPORTED) */
-  XLPK_DTYPE_NVFP4 = 2         /* weights only: e2m1 codes [N][K/2] (element 2j in the low nibble of
+  XLPK_DTYPE_NVFP4 = 2,        /* weights only: e2m1 codes [N][K/2] (element 2j in the low nibble of
                                   byte j), one e4m3 scale per 16 consecutive elements of a row and one
                                   fp32 scale per matrix (xlpk_linear); dense models at batch 1, hidden /
                                   n_q_heads*head_dim / ffn multiples of 128 (else XLPK_ERR_UNSUPPORTED) */
+  XLPK_DTYPE_FP32 = 3          /* operands of the stand-alone operators only (not a weight or cache type) */
 } xlpk_dtype;
 
 /* Model and launch shape.  All widths are element counts.
@@ -426,6 +427,153 @@ const char* xlpk_last_cuda_error(void);
  * section 6.2, warp specialisation). */
 xlpk_status xlpk_tc_gemm_tile(const void* w_dev, int32_t n, int32_t k, const float* x_dev, float* y_dev,
                               void* stream);
+
+/* ---- Stand-alone operators around the decode.  They take no handle: operands
+ * are device pointers on the current device, every call is asynchronous on
+ * `stream`, allocates nothing and may be recorded by stream capture.  Workspaces
+ * belong to one call until it has finished on the GPU: calls whose executions may
+ * overlap (other streams, two captured graphs) need one each.  What only the
+ * device can see (a page outside the pool, a length past the table) is written
+ * to a status word that the caller owns, zeroes and reads. */
+
+/* Attention of one new token per sequence over its KV cache.
+ *     out[b][i] = sum_t p_t v[t],   p = softmax over visible t of scale * q[b][i] . k[t]
+ * where query head i reads kv head i / (n_q_heads / n_kv_heads), the cache holds
+ * n = seq_lens[b] positions and t is visible if t < n and (window == 0, or
+ * t >= n - window, or t < sinks).  With k_new / v_new the call first stores them,
+ * rounded as a decode rounds (bf16, or the e4m3 code of x / scale, to nearest even,
+ * saturated), as the row of position n - 1, and attends over what it stored.
+ *  - head_dim 64 or 128; any n_q_heads / n_kv_heads up to 16; q, k_new, v_new and
+ *    out are all io_dtype: XLPK_DTYPE_BF16 or XLPK_DTYPE_FP32.  Sums, softmax
+ *    statistics and lse are fp32.
+ *  - The cache is the one of xlpk_kv for one layer, in any order whose rows of
+ *    head_dim entries are contiguous.  Paged: row t of kv head h of sequence b is
+ *    at page * page_stride + h * head_stride + (t % page_size) * pos_stride of k_dev
+ *    and v_dev, page = page_table_dev[b * table_stride + t / page_size].  Any
+ *    page_size >= 1.  Contiguous: page_table_dev NULL, page b is sequence b
+ *    (n_pages = n_seqs) and page_size its capacity, table_cols 1.
+ *  - Strides count elements.  q, new and out rows are head_dim contiguous
+ *    elements.  Every pointer, and every stride in bytes, is a multiple of 16
+ *    (else XLPK_ERR_INVALID_ARG; lse_dev, seq_lens_dev, page_table_dev and
+ *    status_dev: of 4).
+ *  - n = 0: the output row is zero, lse -inf, nothing is stored.
+ *  - q and the visible entries are finite; what stands elsewhere may be anything.
+ *  - Rows of the cache that no sequence sees are not read: pages a window has
+ *    passed may be gone from the table.  A visible position whose page lies
+ *    outside [0, n_pages), or a length outside [0, table_cols * page_size], makes
+ *    that sequence's output NaN and *status_dev (may be NULL)
+ *    XLPK_ERR_INVALID_ARG; nothing outside the pool is touched.
+ *  - A sequence whose new row is stored must be the only one in the call that
+ *    reads that row.
+ * The result is the same bits from call to call on one GPU model.
+ * workspace_dev: 16-byte aligned, at least
+ * xlpk_decode_attention_workspace(args) bytes, contents irrelevant. */
+typedef struct xlpk_attention_args {
+  const void* q_dev;               /* [n_seqs][n_q_heads][head_dim] */
+  const void* k_new_dev;           /* [n_seqs][n_kv_heads][head_dim], or NULL */
+  const void* v_new_dev;           /* NULL exactly if k_new_dev is */
+  void* k_dev;                     /* the cache (written only with k_new_dev) */
+  void* v_dev;
+  const int32_t* page_table_dev;   /* [n_seqs][table_cols], or NULL: contiguous */
+  const int32_t* seq_lens_dev;     /* [n_seqs] */
+  void* out_dev;                   /* [n_seqs][n_q_heads][head_dim] */
+  float* lse_dev;                  /* [n_seqs][n_q_heads] natural log of the softmax's denominator, or NULL */
+  int32_t* status_dev;             /* one word, or NULL */
+  int64_t q_seq_stride, q_head_stride;
+  int64_t new_k_seq_stride, new_k_head_stride, new_v_seq_stride, new_v_head_stride;
+  int64_t out_seq_stride, out_head_stride;
+  int64_t k_page_stride, k_head_stride, k_pos_stride;
+  int64_t v_page_stride, v_head_stride, v_pos_stride;
+  int64_t table_stride;            /* entries from one sequence's table row to the next */
+  int32_t n_seqs, n_q_heads, n_kv_heads, head_dim;
+  int32_t n_pages, page_size, table_cols;
+  int32_t io_dtype, kv_dtype;      /* kv_dtype: XLPK_DTYPE_BF16 or XLPK_DTYPE_FP8_E4M3 */
+  int32_t window, sinks;           /* 0 window: every position is visible */
+  float scale;                     /* finite, > 0 */
+  float k_scale, v_scale;          /* e4m3 cache: powers of two in [2^-24, 2^24]; else ignored */
+} xlpk_attention_args;
+
+int64_t xlpk_decode_attention_workspace(const xlpk_attention_args* args);   /* 0 for a bad shape */
+xlpk_status xlpk_decode_attention(const xlpk_attention_args* args, void* workspace_dev, int64_t workspace_bytes,
+                                  void* stream);
+
+/* The pages of a paged cache and who holds them.  The pools are those of
+ * xlpk_kv with any page size: K and V each [n_layers][n_pages][n_kv_heads]
+ * [page_size][row_bytes].  Row r of the table is a sequence of seq_lens[r]
+ * positions; an entry of -1 holds no page.  refs[p] counts the entries that
+ * name page p, plus the references that the caller keeps besides (a prefix held
+ * for later); a page with refs 0 is free.  Table, lengths and counts are device
+ * memory that the calls update in place, so a loop of them with decode calls
+ * needs no host copy.  Fresh pages are always the lowest-numbered free ones, in
+ * row order: results do not depend on timing.
+ * A call that cannot be done changes nothing and writes why to *status_dev:
+ * XLPK_ERR_OOM (too few free pages), XLPK_ERR_KV_FULL (a row past its table) or
+ * XLPK_ERR_INVALID_ARG (a length, parent, or entry out of range).  While
+ * *status_dev is not XLPK_OK every call on the pool does nothing, until the
+ * caller has zeroed it. */
+typedef struct xlpk_page_pool {
+  void* k_dev;                     /* 16-byte aligned */
+  void* v_dev;
+  int32_t* page_table_dev;         /* [rows][cols] */
+  int32_t* seq_lens_dev;           /* [rows] */
+  int32_t* refs_dev;               /* [n_pages] */
+  int32_t* status_dev;             /* one word */
+  int32_t n_layers, n_pages, n_kv_heads, page_size;
+  int32_t row_bytes;               /* bytes of one position of one kv head, a multiple of 16 */
+  int32_t rows, cols;              /* rows <= 1024 */
+} xlpk_page_pool;
+
+/* Bytes of the workspace of xlpk_pages_fork and xlpk_pages_compact (16-byte aligned). */
+int64_t xlpk_pages_workspace(const xlpk_page_pool* pool);
+
+/* Row r becomes what row parents[r] was (-1: empty), for all rows at once: a
+ * beam search's reordering, a prompt fanned out, finished rows freed.  Children
+ * share the parent's full pages.  One child, the row itself if it is its own
+ * parent, else the lowest-numbered, takes over the partly filled page and any
+ * pages reserved behind it; every other child gets a fresh page with a copy of
+ * the filled positions of every layer.  References of rows without a child are
+ * dropped; pages this call frees are not reused before the next one. */
+xlpk_status xlpk_pages_fork(const xlpk_page_pool* pool, const int32_t* parents_dev, void* workspace_dev,
+                            int64_t workspace_bytes, void* stream);
+
+/* Each row gets the pages it lacks to hold positions [seq_lens[r], want[r]).
+ * Lengths are not changed. */
+xlpk_status xlpk_pages_reserve(const xlpk_page_pool* pool, const int32_t* want_dev, void* stream);
+
+/* Give back the pages that a sliding window has passed: those whose positions
+ * are all < seq_lens[r] - window and >= sinks.  window 0: none. */
+xlpk_status xlpk_pages_trim(const xlpk_page_pool* pool, int32_t window, int32_t sinks, void* stream);
+
+/* Move the live pages (refs > 0) to the numbers below their count: the k-th
+ * free page below it takes the contents of the k-th live page at or above it.
+ * Table and counts follow.  remap_dev [n_pages] (or NULL): the new number of
+ * every page, -1 for a free one, for references that the caller keeps. */
+xlpk_status xlpk_pages_compact(const xlpk_page_pool* pool, int32_t* remap_dev, void* workspace_dev,
+                               int64_t workspace_bytes, void* stream);
+
+/* Copy page src[i] to page dst[i], all layers, i < n (host arrays, read during
+ * the call).  No page may be a destination twice, or a source and a
+ * destination (XLPK_ERR_INVALID_ARG).  Table, lengths and counts stay. */
+xlpk_status xlpk_pages_copy(const xlpk_page_pool* pool, const int32_t* src_host, const int32_t* dst_host, int32_t n,
+                            void* stream);
+
+/* Log probabilities of given tokens under rows of logits, as a decode writes
+ * them (xlpk_decode_io::logits_dev):
+ *     logprob[r] = x[r][tokens[r]] - lse(x[r]),   entropy[r] = -sum_j p_j log p_j,
+ *     rank[r] = the tokens before tokens[r] in descending order of x (ties: the lower id first),
+ *     top_ids / top_logprobs [r][k] = the first top_k tokens of that order.
+ *  - logits: `dtype` XLPK_DTYPE_FP32 or XLPK_DTYPE_BF16, row r at logits_dev + r *
+ *    row_stride elements, any alignment of the element type; arithmetic is fp32.
+ *  - 0 <= top_k <= min(64, vocab); entropy_dev, rank_dev and, with top_k = 0, the
+ *    top pointers may be NULL.
+ *  - Masked tokens are -inf (or the type's lowest value): probability 0.  A row of
+ *    nothing but -inf has logprob and top_logprobs -inf and entropy 0.  A row with
+ *    +inf or NaN has NaN for all of them (NaN sorts before +inf).
+ *  - A token outside [0, vocab) (padding) gives logprob NaN and rank -1. */
+xlpk_status xlpk_token_logprobs(const void* logits_dev, int32_t dtype, int64_t rows, int32_t vocab,
+                                int64_t row_stride, const int32_t* tokens_dev, int32_t top_k, float* logprob_dev,
+                                float* entropy_dev, int32_t* rank_dev, int32_t* top_ids_dev, float* top_logprobs_dev,
+                                void* stream);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,7 @@ XLPK_NOALLOC_SCRATCH_BYTES = 8 << 20
 XLPK_DTYPE_BF16 = 0
 XLPK_DTYPE_FP8_E4M3 = 1
 XLPK_DTYPE_NVFP4 = 2
+XLPK_DTYPE_FP32 = 3
 
 XLPK_FLAG_NO_FUSED_FFN = 1
 XLPK_FLAG_NO_TENSOR_CORES = 2
@@ -73,6 +74,24 @@ class xlpk_info(C.Structure):
                 ("workspace_bytes", C.c_int64), ("weight_bytes_per_step", C.c_int64)]
 
 
+class xlpk_attention_args(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "q_dev", "k_new_dev", "v_new_dev", "k_dev", "v_dev", "page_table_dev", "seq_lens_dev", "out_dev", "lse_dev",
+        "status_dev")] + [(n, C.c_int64) for n in (
+            "q_seq_stride", "q_head_stride", "new_k_seq_stride", "new_k_head_stride", "new_v_seq_stride",
+            "new_v_head_stride", "out_seq_stride", "out_head_stride", "k_page_stride", "k_head_stride", "k_pos_stride",
+            "v_page_stride", "v_head_stride", "v_pos_stride", "table_stride")] + [(n, C.c_int32) for n in (
+                "n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "n_pages", "page_size", "table_cols", "io_dtype",
+                "kv_dtype", "window", "sinks")] + [(n, C.c_float) for n in ("scale", "k_scale", "v_scale")]
+
+
+class xlpk_page_pool(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k_dev", "v_dev", "page_table_dev", "seq_lens_dev", "refs_dev",
+                                          "status_dev")] + [(n, C.c_int32) for n in (
+                                              "n_layers", "n_pages", "n_kv_heads", "page_size", "row_bytes", "rows",
+                                              "cols")]
+
+
 # name -> (restype, argtypes); every symbol the header declares
 SIGNATURES = {
     "xlpk_create": (C.c_int32, [C.POINTER(xlpk_config), C.POINTER(xlpk_weights),
@@ -98,6 +117,17 @@ SIGNATURES = {
     "xlpk_status_string": (C.c_char_p, [C.c_int32]),
     "xlpk_last_cuda_error": (C.c_char_p, []),
     "xlpk_tc_gemm_tile": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "xlpk_decode_attention_workspace": (C.c_int64, [C.POINTER(xlpk_attention_args)]),
+    "xlpk_decode_attention": (C.c_int32, [C.POINTER(xlpk_attention_args), C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_workspace": (C.c_int64, [C.POINTER(xlpk_page_pool)]),
+    "xlpk_pages_fork": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_reserve": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p]),
+    "xlpk_pages_trim": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_int32, C.c_int32, C.c_void_p]),
+    "xlpk_pages_compact": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_copy": (C.c_int32, [C.POINTER(xlpk_page_pool), C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
+                                    C.c_void_p]),
+    "xlpk_token_logprobs": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
+                                        C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
 }
 
 

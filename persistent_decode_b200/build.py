@@ -14,9 +14,10 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "xlpk.cu")
 KERNELS = os.path.join(HERE, "csrc", "kernels.cu")
 KERNEL_UNITS = 11   # kKernelUnits in csrc/kernels.h
+OPERATORS = [os.path.join(HERE, "csrc", f) for f in ("attention.cu", "pages.cu", "logprobs.cu")]
 DEPS = [os.path.join(HERE, "csrc", f) for f in ("xlpk.cu", "kernels.cu", "kernels.h", "engine.cuh", "tcgen05.cuh",
-                                                "tc_tile.cuh", "params.h")] + \
-    [os.path.join(ROOT, "include", "xlpk.h")]
+                                                "tc_tile.cuh", "params.h", "errors.h")] + \
+    OPERATORS + [os.path.join(ROOT, "include", "xlpk.h")]
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libxlpk.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -52,6 +53,9 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str = Non
     common = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-Xfatbin", "-compress-all",
               "-I", os.path.join(ROOT, "include"), *[f"-D{d}" for d in defines]]
     jobs = [([nvcc, *common, "-c", SRC, "-o", os.path.join(obj_dir, "xlpk.o")], os.path.join(obj_dir, "xlpk.o"))]
+    for src in OPERATORS:
+        o = os.path.join(obj_dir, os.path.basename(src)[:-3] + ".o")
+        jobs.append(([nvcc, *common, "-c", src, "-o", o], o))
     for u in range(KERNEL_UNITS):
         o = os.path.join(obj_dir, f"kernels{u}.o")
         jobs.append(([nvcc, *common, f"-DXLPK_UNIT={u}", "-c", KERNELS, "-o", o], o))

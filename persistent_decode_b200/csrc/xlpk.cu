@@ -26,25 +26,55 @@
 
 #include "../../include/xlpk.h"
 #include "engine.cuh"
+#include "errors.h"
 #include "kernels.h"
 #include "params.h"
 
 using namespace xlpk;
 
-namespace {
+static thread_local std::string g_cuda_err;
 
-thread_local std::string g_cuda_err;
+namespace xlpk {
 
 xlpk_status cuda_fail(cudaError_t e, const char* what) {
-  g_cuda_err = std::string(what) + ": " + cudaGetErrorString(e);
-  return e == cudaErrorMemoryAllocation ? XLPK_ERR_OOM : XLPK_ERR_CUDA;
+  const xlpk_status st = e == cudaErrorMemoryAllocation ? XLPK_ERR_OOM : XLPK_ERR_CUDA;
+  try {
+    g_cuda_err = std::string(what) + ": " + cudaGetErrorString(e);
+  } catch (...) {
+    g_cuda_err.clear();
+  }
+  return st;
 }
 
-#define XLPK_CUDA(call)                               \
-  do {                                                \
-    cudaError_t e_ = (call);                          \
-    if (e_ != cudaSuccess) return cuda_fail(e_, #call); \
-  } while (0)
+xlpk_status refuse(xlpk_status st, const char* why) noexcept {
+  try {
+    g_cuda_err = why;
+  } catch (...) {
+    g_cuda_err.clear();
+  }
+  return st;
+}
+
+xlpk_status current_sms(int* sms) {
+  static std::atomic<int> known[64];   // 0: not asked yet, < 0: not an sm_100
+  int dev = -1;
+  XLPK_CUDA(cudaGetDevice(&dev));
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    int major = 0;
+    XLPK_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    XLPK_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
+    if (major != 10) n = -1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  if (n < 0) return refuse(XLPK_ERR_UNSUPPORTED, "device is not sm_100");
+  *sms = n;
+  return XLPK_OK;
+}
+
+}  // namespace xlpk
+
+namespace {
 
 struct PackJob {
   const uint8_t* src;   // source row

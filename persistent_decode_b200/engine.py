@@ -11,6 +11,7 @@ from typing import Dict, Optional
 from . import _abi
 
 _LIB = None
+SCORE_BYTES = 256 << 20   # Engine.score's logits buffer
 
 
 def get_lib():
@@ -30,9 +31,10 @@ lib = _LazyLib()
 
 
 class XlpkError(RuntimeError):
-    def __init__(self, status: int, what: str):
+    def __init__(self, status: int, what: str, detail: Optional[str] = None):
         msg = lib.xlpk_status_string(status).decode()
-        detail = lib.xlpk_last_cuda_error().decode()
+        if detail is None:
+            detail = lib.xlpk_last_cuda_error().decode()
         super().__init__(f"{what}: {msg}" + (f" ({detail})" if detail else ""))
         self.status = status
 
@@ -230,6 +232,39 @@ class Engine:
         _check(lib.xlpk_verify(self.h, _ptr(drafts), int(drafts.numel()), _ptr(argmax_out), C.byref(n),
                                C.byref(io) if io is not None else None, _stream_handle(stream)), "xlpk_verify")
         return int(n.value)
+
+    def score(self, tokens, top_k: int = 0):
+        """Log probabilities of given tokens: feed `tokens` (int32 CUDA tensor [n][B])
+        after the pending ones, as a decode forced to them, and return their
+        ops.TokenLogprobs ([n][B], alternatives [n][B][top_k]).  The state moves on by
+        n positions; the last tokens are pending.  Logits live in a buffer of at most
+        SCORE_BYTES (or one step), whatever n."""
+        import torch
+        from .ops import TokenLogprobs, token_logprobs
+        n = int(tokens.shape[0])
+        tokens = tokens.contiguous()
+        dev, V = tokens.device, self.cfg.vocab
+        most = max(1, min(n, SCORE_BYTES // (4 * self.B * V)))
+        logits = torch.empty(most, self.B, V, dtype=torch.float32, device=dev)
+        out = torch.empty(most, self.B, dtype=torch.int32, device=dev)
+        parts = []
+        for s in range(0, n, most):
+            t = tokens[s:s + most]
+            self.decode(t.shape[0], out, forced=t, logits=logits)
+            parts.append(token_logprobs(logits[:t.shape[0]], t, top_k))
+        if not parts:
+            return token_logprobs(logits[:0], tokens, top_k)
+        return TokenLogprobs(*(torch.cat(f) if f[0] is not None else None for f in zip(*parts)))
+
+    def page_pool(self, seq_lens, refs=None):
+        """The paged cache's ops.PagePool: `seq_lens` int32 CUDA tensor [B] of positions
+        in the cache.  Its calls change the table that later decodes read; name the
+        lengths they left to set_state."""
+        from .ops import PagePool
+        _, k, v, table = self._refs
+        if table is None:
+            raise ValueError("the cache is contiguous: it has no pages")
+        return PagePool(k, v, table, seq_lens, refs)
 
     # ---- device-resident request loop (xlpk_serve_*)
 
