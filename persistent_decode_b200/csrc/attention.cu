@@ -1,9 +1,12 @@
 // xlpk_decode_attention: attention of one new token per sequence over its KV
 // cache (include/xlpk.h has the definition).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -16,111 +19,669 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 256;
+constexpr int kTile = 16;   // positions a warp takes at a time
 
-__device__ inline float load_io(const void* p, long long i, int io) {
-  return io == XLPK_DTYPE_FP32 ? static_cast<const float*>(p)[i]
-                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+struct Args {
+  xlpk_attention_args a;
+  float* parts;     // [CTAs][2] slots of partial results
+  int4* joins;      // [CTAs] (sequence, kv head, last CTA, -) of the segment that CTA begins and another ends; .x < 0: none
+};
+
+// The tiles of one sequence: those that hold a visible position.
+struct Seq {
+  int n;       // positions
+  int lo;      // the window's first position; the first tokens before it are visible too
+  int head;    // tiles of first tokens, before the gap
+  int skip;    // tiles of the gap
+  int tiles;   // all but the gap's
+};
+__device__ inline Seq seq_of(const xlpk_attention_args& a, int b) {
+  Seq s;
+  s.n = a.seq_lens_dev[b];
+  if (s.n < 0 || s.n > static_cast<long long>(a.table_cols) * a.page_size) s.n = 0;
+  s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
+  s.head = (min(a.sinks, s.lo) + kTile - 1) / kTile;
+  s.skip = max(s.lo / kTile - s.head, 0);
+  s.tiles = (s.n + kTile - 1) / kTile - s.skip;
+  return s;
 }
-__device__ inline void store_io(void* p, long long i, int io, float v) {
-  if (io == XLPK_DTYPE_FP32)
-    static_cast<float*>(p)[i] = v;
+__device__ inline int tile_pos(const Seq& s, int i) { return (i < s.head ? i : i + s.skip) * kTile; }
+__device__ inline bool visible(const xlpk_attention_args& a, const Seq& s, int t) {
+  return t < s.n && (t >= s.lo || t < a.sinks);
+}
+
+// One stretch of consecutive tiles in the order (sequence, kv head, tile), cut
+// at segment borders: a segment is one kv head of one sequence.
+struct Walk {
+  int b, h, i, end;      // tiles [i, end) of segment (b, h)
+  long long left;        // tiles after them
+  Seq s;
+};
+__device__ inline void walk_cut(Walk& w, long long n) {
+  const long long e = w.i + n;
+  w.end = e < w.s.tiles ? static_cast<int>(e) : w.s.tiles;
+  w.left = e - w.end;
+}
+// To the next segment (left > 0).
+__device__ inline void walk_next(const xlpk_attention_args& a, Walk& w) {
+  if (++w.h == a.n_kv_heads) {
+    w.h = 0;
+    do w.s = seq_of(a, ++w.b);
+    while (w.s.tiles == 0);
+  }
+  w.i = 0;
+  walk_cut(w, w.left);
+}
+
+template <int D_, bool KV8_, bool WIDE_, bool IO32_>
+struct Shape {
+  static constexpr int D = D_;
+  static constexpr bool KV8 = KV8_;      // e4m3 cache, fp16 operands; else bf16
+  static constexpr bool WIDE = WIDE_;    // 9 to 16 query heads per kv head; else up to 8
+  static constexpr bool IO32 = IO32_;
+  static constexpr int E = KV8 ? 1 : 2;
+  static constexpr int ROWS = WIDE ? 16 : 8;
+  // what one lane copies of a cache row: a K row is read by the 4 lanes of a quad in 16-byte
+  // chunks, a V row by the 8 lanes that share a quad position
+  static constexpr int KC = D * E / 64;
+  static constexpr int VB = D * E / 8 >= 16 ? 16 : 8;
+  static constexpr int VC = D * E / 8 / VB;
+  static constexpr int KBYTES = 2 * KC * 512, STAGE = KBYTES + 4 * VC * VB * 32;
+  static constexpr int MERGE = kWarps * ROWS * (D + 2) * 4;
+  static constexpr int FIT = (232448 - 1024 - MERGE) / (STAGE * kWarps);
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  static constexpr int SMEM = STAGES * STAGE * kWarps + MERGE;
+  static constexpr int QT = IO32 ? (KV8 ? 2 : 3) : 1;   // terms of q
+  static constexpr int PT = IO32 && !KV8 ? 3 : 2;       // terms of p
+  static constexpr int QR = D / 8;                      // registers of one term of one row
+  static constexpr int SHIFT = KV8 ? 10 : 0;            // p is held times 2^SHIFT
+  static constexpr int SLOT = ROWS * (D + 2);           // floats of a partial result
+};
+
+__device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                           bool f16) {
+  if (f16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ inline float load_kv(const void* p, long long i, int kv, float scale) {
-  if (kv == XLPK_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  __nv_fp8_e4m3 c;
-  c.__x = static_cast<const uint8_t*>(p)[i];
-  return static_cast<float>(c) * scale;
-}
-// Stores x as a cache entry and returns the value the entry stands for.
-__device__ inline float round_kv(void* p, long long i, int kv, float scale, float x, bool store) {
-  if (kv == XLPK_DTYPE_BF16) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(x);
-    if (store) static_cast<__nv_bfloat16*>(p)[i] = b;
-    return __bfloat162float(b);
+
+// The next 16-bit term of x and y as a register; x and y keep the remainders.
+template <bool F16>
+__device__ inline uint32_t term(float& x, float& y) {
+  uint32_t r;
+  if (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    x -= __low2float(h), y -= __high2float(h);
+    r = *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    x -= __low2float(h), y -= __high2float(h);
+    r = *reinterpret_cast<const uint32_t*>(&h);
   }
-  __nv_fp8_e4m3 c(x / scale);
-  if (store) static_cast<uint8_t*>(p)[i] = c.__x;
-  return static_cast<float>(c) * scale;
+  return r;
 }
 
-// One block per (sequence, query head), its warps stepping through the visible
-// positions with an online softmax each, merged at the end.
-constexpr int kWarps = 4;
+// Two e4m3 codes (the low 16 bits) as two fp16 values, exactly.
+__device__ inline uint32_t widen(uint32_t codes) {
+  uint32_t r;
+  asm("{ .reg .b16 l; mov.b32 {l, _}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(codes));
+  return r;
+}
 
-__global__ void attention_kernel(const xlpk_attention_args a) {
-  const int h = blockIdx.x, b = blockIdx.y, g = a.n_q_heads / a.n_kv_heads, kh = h / g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = a.head_dim / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][128];
-  __shared__ int bad_page;
-  if (threadIdx.x == 0) bad_page = 0;
-  __syncthreads();
-  const long long cap = static_cast<long long>(a.table_cols) * a.page_size;
-  int n = a.seq_lens_dev[b];
-  bool bad = n < 0 || n > cap;
-  if (bad) n = 0;
-  const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
-  const int first = a.sinks < lo ? a.sinks : lo;   // [0, first) and [lo, n)
-  const int count = first + (n - lo);
-  float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0;
-  for (int i = 0; i < per; ++i)
-    q[i] = load_io(a.q_dev, b * a.q_seq_stride + h * a.q_head_stride + lane + 32 * i, a.io_dtype);
-  const float s2 = a.scale * kLog2e;
-  for (int v = warp; v < count; v += kWarps) {
-    const int t = v < first ? v : lo + (v - first);
-    const int j = t / a.page_size, r = t - j * a.page_size;
-    const long long page = a.page_table_dev ? a.page_table_dev[b * a.table_stride + j] : b;
-    if (page < 0 || page >= a.n_pages) {
-      bad_page = 1;
-      continue;
+template <bool IO32, int N>
+__device__ inline void load_row(const void* base, long long at, float (&x)[N]) {
+  if (IO32) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 v = p[i];
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
     }
-    const long long ko = page * a.k_page_stride + kh * a.k_head_stride + r * a.k_pos_stride;
-    const long long vo = page * a.v_page_stride + kh * a.v_head_stride + r * a.v_pos_stride;
-    const bool fresh = a.k_new_dev && t == n - 1;
-    float s = 0, vv[4];
-    for (int i = 0; i < per; ++i) {
-      const int e = lane + 32 * i;
-      float k;
-      if (fresh) {
-        k = round_kv(a.k_dev, ko + e, a.kv_dtype, a.k_scale,
-                     load_io(a.k_new_dev, b * a.new_k_seq_stride + kh * a.new_k_head_stride + e, a.io_dtype), h == kh * g);
-        vv[i] = round_kv(a.v_dev, vo + e, a.kv_dtype, a.v_scale,
-                         load_io(a.v_new_dev, b * a.new_v_seq_stride + kh * a.new_v_head_stride + e, a.io_dtype), h == kh * g);
-      } else {
-        k = load_kv(a.k_dev, ko + e, a.kv_dtype, a.k_scale);
-        vv[i] = load_kv(a.v_dev, vo + e, a.kv_dtype, a.v_scale);
+  } else {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint4 v = p[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
-      s += q[i] * k;
     }
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
-    s *= s2;
-    const float mn = s > m || s != s ? s : m;   // NaN stays
-    const float w = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    l = l * w + p;
-    for (int i = 0; i < per; ++i) o[i] = o[i] * w + p * vv[i];
-    m = mn;
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-  for (int i = 0; i < per; ++i) so[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  if (threadIdx.x >= a.head_dim) return;
-  float M = -INFINITY, L = 0, O = 0;
-  for (int w = 0; w < kWarps; ++w) M = sm[w] > M || sm[w] != sm[w] ? sm[w] : M;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = M == -INFINITY ? 0.f : exp2f(sm[w] - M);
-    L += sl[w] * f;
-    O += so[w][threadIdx.x] * f;
+}
+
+template <bool IO32>
+__device__ inline void store_out(void* base, long long at, float4 v) {
+  if (IO32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = v;
+  } else {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(v.x, v.y), h = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&l), *reinterpret_cast<const uint32_t*>(&h));
   }
-  bad = bad || bad_page;
-  const float nan = __int_as_float(0x7fffffff);
-  const float out = bad ? nan : L == 0 ? 0.f : O / L;
-  store_io(a.out_dev, b * a.out_seq_stride + h * a.out_head_stride + threadIdx.x, a.io_dtype, out);
-  if (threadIdx.x == 0) {
+}
+
+// N elements of a new row as cache entries: `bytes` of them in w.
+template <bool KV8, int N>
+__device__ inline void round_row(const float (&x)[N], float inv_scale, uint32_t* w) {
+  if (KV8) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv_scale, x[4 * i + 1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv_scale, x[4 * i + 3] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+      w[i] = l | h << 16;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
+
+template <int BYTES>
+__device__ inline void copy_async(uint32_t dst, const void* src, bool real) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real ? 8 : 0) : "memory");
+}
+
+// 2^x to 2^-22, 0 for -inf.
+__device__ inline float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ inline float lse_of(float m, float l, int shift) { return l == 0 ? -INFINITY : (m - shift) * kLn2 + logf(l); }
+
+template <class S>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args args) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up meanwhile; it waits for this grid's end
+  __shared__ long long scan[kWarps], start[2];
+  const xlpk_attention_args& a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int group = a.n_q_heads / a.n_kv_heads;
+  constexpr int D = S::D;
+
+  // ---- this CTA's even share [x0, x1) of all tiles, and the segment it begins in
+  Walk w{};
+  long long count;   // its tiles
+  int ctas;          // CTAs that have any
+  long long tiles_in_all;
+  long long x0;
+  {
+    const int per = (a.n_seqs + kThreads - 1) / kThreads, b0 = min(static_cast<int>(threadIdx.x) * per, a.n_seqs),
+              b1 = min(b0 + per, a.n_seqs);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_of(a, b).tiles;
+    long long sum = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += y;
+    }
+    if (lane == 31) scan[warp] = sum;
+    __syncthreads();
+    long long total = 0, before = sum - mine;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += scan[i];
+      total += scan[i];
+    }
+    total *= a.n_kv_heads;
+    tiles_in_all = total;
+    ctas = total < gridDim.x ? static_cast<int>(total) : gridDim.x;
+    const bool any = static_cast<int>(blockIdx.x) < ctas;
+    x0 = any ? blockIdx.x * total / ctas : 0;
+    count = any ? (blockIdx.x + 1) * total / ctas - x0 : 0;
+    if (any && mine > 0 && before * a.n_kv_heads <= x0 && x0 < (before + mine) * a.n_kv_heads) {
+      int b = b0;
+      long long off = x0 - before * a.n_kv_heads;
+      for (;; ++b) {
+        const long long seg = static_cast<long long>(seq_of(a, b).tiles) * a.n_kv_heads;
+        if (off < seg) break;
+        off -= seg;
+      }
+      start[0] = b;
+      start[1] = off;
+    }
+    // who joins the pieces of the segment that this CTA begins and does not end is said at its end
+    if (threadIdx.x == 0) args.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    if (any) {
+      w.b = static_cast<int>(start[0]);
+      w.s = seq_of(a, w.b);
+      w.h = static_cast<int>(start[1] / w.s.tiles);
+      w.i = static_cast<int>(start[1] - static_cast<long long>(w.h) * w.s.tiles);
+      walk_cut(w, count);
+    }
+  }
+
+  // ---- rows without positions
+  for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
+    const int n = a.seq_lens_dev[b];
+    const bool bad = n < 0 || n > static_cast<long long>(a.table_cols) * a.page_size;
+    if (n != 0 && !bad) continue;
+    const float v = bad ? __int_as_float(0x7fffffff) : 0.f;
+    for (int i = threadIdx.x * 4; i < a.n_q_heads * D; i += kThreads * 4)
+      store_out<S::IO32>(a.out_dev, b * a.out_seq_stride + i / D * a.out_head_stride + i % D, make_float4(v, v, v, v));
     if (a.lse_dev)
-      a.lse_dev[static_cast<long long>(b) * a.n_q_heads + h] = bad ? nan : L == 0 ? -INFINITY : M * kLn2 + logf(L);
-    if (bad && a.status_dev) *a.status_dev = XLPK_ERR_INVALID_ARG;
+      for (int i = threadIdx.x; i < a.n_q_heads; i += kThreads)
+        a.lse_dev[static_cast<long long>(b) * a.n_q_heads + i] = bad ? v : -INFINITY;
+    if (bad && a.status_dev && threadIdx.x == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
   }
+  if (count == 0) return;
+
+  // ---- the warp's queue of tiles in shared memory.  Every lane copies exactly the bytes that
+  // it multiplies, so a lane's own wait is the only one: no barrier, no shared index.
+  const uint32_t queue = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::STAGES * S::STAGE;
+  const uint8_t* queue_at = smem + warp * S::STAGES * S::STAGE;
+  Walk f = w;            // the tile that is fetched next
+  f.i += warp;
+  int page_f = -1, in_f = 0, bad_stages = 0;
+  bool more = true;
+  // lanes 0..15 look up the row of one position each
+  auto settle = [&]() {
+    while (f.i >= f.end) {
+      if (f.left == 0) {
+        more = false;
+        return;
+      }
+      walk_next(a, f);
+      f.i += warp;
+    }
+    const int pos = tile_pos(f.s, f.i) + (lane & 15);
+    page_f = -1;
+    if (visible(a, f.s, pos)) {
+      const int j = pos / a.page_size;
+      in_f = pos - j * a.page_size;
+      page_f = a.page_table_dev ? a.page_table_dev[f.b * a.table_stride + j] : f.b;
+      if (page_f < 0 || page_f >= a.n_pages) page_f = -2;
+    }
+  };
+  auto fetch = [&](int stage) {
+    if (more) {
+      const bool bad = __any_sync(~0u, page_f == -2);
+      bad_stages = bad ? bad_stages | 1 << stage : bad_stages & ~(1 << stage);
+      const int pos = tile_pos(f.s, f.i);
+      const long long ko = page_f < 0 ? -1 : page_f * a.k_page_stride + in_f * a.k_pos_stride + f.h * a.k_head_stride;
+      const long long vo = page_f < 0 ? -1 : page_f * a.v_page_stride + in_f * a.v_pos_stride + f.h * a.v_head_stride;
+      const int fresh = a.k_new_dev && f.i == f.s.tiles - 1 ? f.s.n - 1 - pos : -1;   // the row of the new token
+      const uint32_t dst = queue + stage * S::STAGE;
+      uint8_t* out = const_cast<uint8_t*>(queue_at) + stage * S::STAGE;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const long long o = __shfl_sync(~0u, ko, g + 8 * r);
+        uint8_t* row = static_cast<uint8_t*>(a.k_dev) + (o < 0 ? 0 : o * S::E);
+        if (fresh == g + 8 * r) {
+#pragma unroll
+          for (int j = 0; j < S::KC; ++j) {
+            constexpr int N = 16 / S::E;
+            float x[N];
+            uint32_t c[4];
+            load_row<S::IO32>(a.k_new_dev, f.b * a.new_k_seq_stride + f.h * a.new_k_head_stride + j * 4 * N + t * N, x);
+            round_row<S::KV8>(x, 1.f / a.k_scale, c);
+            const uint4 v = make_uint4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<uint4*>(out + ((r * S::KC + j) * 32 + lane) * 16) = v;
+            if (o >= 0) *reinterpret_cast<uint4*>(row + j * 64 + t * 16) = v;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < S::KC; ++j)
+            copy_async<16>(dst + ((r * S::KC + j) * 32 + lane) * 16, row + j * 64 + t * 16, o >= 0);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int at = 2 * t + (r & 1) + (r >> 1) * 8;
+        const long long o = __shfl_sync(~0u, vo, at);
+        uint8_t* row = static_cast<uint8_t*>(a.v_dev) + (o < 0 ? 0 : o * S::E);
+        if (fresh == at) {
+#pragma unroll
+          for (int c = 0; c < S::VC; ++c) {
+            constexpr int N = 16 / S::E;   // (a lane of 8 codes rounds 16 and keeps its half)
+            float x[N];
+            uint32_t code[4];
+            const int first = c * 128 / S::E + g * (S::VB / S::E);
+            load_row<S::IO32>(a.v_new_dev, f.b * a.new_v_seq_stride + f.h * a.new_v_head_stride + first / N * N, x);
+            round_row<S::KV8>(x, 1.f / a.v_scale, code);
+            uint8_t* q = out + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB;
+            if (S::VB == 16) {
+              const uint4 v = make_uint4(code[0], code[1], code[2], code[3]);
+              *reinterpret_cast<uint4*>(q) = v;
+              if (o >= 0) *reinterpret_cast<uint4*>(row + c * 128 + g * 16) = v;
+            } else {
+              const uint2 v = first % N ? make_uint2(code[2], code[3]) : make_uint2(code[0], code[1]);
+              *reinterpret_cast<uint2*>(q) = v;
+              if (o >= 0) *reinterpret_cast<uint2*>(row + g * 8) = v;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < S::VC; ++c)
+            copy_async<S::VB>(dst + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB, row + c * 128 + g * S::VB, o >= 0);
+        }
+      }
+      if (bad && a.status_dev && lane == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
+      f.i += kWarps;
+      settle();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  settle();
+#pragma unroll 1
+  for (int i = 0; i < S::STAGES; ++i) fetch(i);
+
+  float* const merge = reinterpret_cast<float*>(smem + S::STAGES * S::STAGE * kWarps);
+  float* const merge_m = merge + kWarps * S::ROWS * D;
+  float* const merge_l = merge_m + kWarps * S::ROWS;
+  const float s2 = a.scale * kLog2e * (S::KV8 ? a.k_scale : 1.f);
+  long long x = x0;   // the segment's first tile here
+  int stage = 0;
+  for (;;) {
+    // ---- q of the segment's heads, as terms
+    uint32_t q[S::WIDE ? 2 : 1][S::QT][S::QR];
+    float rs[S::WIDE ? 2 : 1];
+#pragma unroll
+    for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
+      float v[D / 4];
+      const int head = g + 8 * r;
+      if (head < group) {
+        constexpr int N = 16 / S::E;
+#pragma unroll
+        for (int j = 0; j < S::KC; ++j)
+          load_row<S::IO32>(a.q_dev, w.b * a.q_seq_stride + (w.h * group + head) * a.q_head_stride + j * 4 * N + t * N,
+                            *reinterpret_cast<float(*)[N]>(v + j * N));
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) v[i] = 0.f;
+      }
+      rs[r] = s2;
+      if (S::KV8) {
+        // fp16 terms: the row is scaled by the power of two that brings its largest entry to
+        // [2^10, 2^11), where 11 bits of it, and what they leave, are held far below 2^-24 of it
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = top > 0x1p-100f && top < 0x1p100f ? 10 - ilogbf(top) : 0;
+        const float up = ldexpf(1.f, e);
+        rs[r] *= ldexpf(1.f, -e);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) v[i] *= up;
+      }
+#pragma unroll
+      for (int i = 0; i < S::QR; ++i)
+#pragma unroll
+        for (int k = 0; k < S::QT; ++k) q[r][k][i] = term<S::KV8>(v[2 * i], v[2 * i + 1]);
+    }
+
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    bool bad = false;
+
+    for (int i = w.i + warp; i < w.end; i += kWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
+      const uint8_t* at = queue_at + stage * S::STAGE;
+      // ---- scores: positions are the columns
+      float s[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < S::KC; ++j) {
+          const uint4 k4 = *reinterpret_cast<const uint4*>(at + ((nt * S::KC + j) * 32 + lane) * 16);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+          uint32_t kb[8];
+          constexpr int NB = S::KV8 ? 8 : 4;
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            if (S::KV8)
+              kb[2 * i2] = widen(kw[i2]), kb[2 * i2 + 1] = widen(kw[i2] >> 16);
+            else
+              kb[i2] = kw[i2];
+          }
+#pragma unroll
+          for (int p = 0; p < NB; p += 2) {
+            const int c = j * NB + p;
+            if (S::WIDE) {
+#pragma unroll
+              for (int k = 0; k < S::QT; ++k)
+                mma(s[nt], q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[p], kb[p + 1], S::KV8);
+            } else {
+              if (S::QT > 1)
+                mma(s[nt], q[0][0][c], q[0][S::QT > 1][c], q[0][0][c + 1], q[0][S::QT > 1][c + 1], kb[p], kb[p + 1], S::KV8);
+              else
+                mma(s[nt], q[0][0][c], 0, q[0][0][c + 1], 0, kb[p], kb[p + 1], S::KV8);
+              if (S::QT > 2) mma(s[nt], q[0][S::QT - 1][c], 0, q[0][S::QT - 1][c + 1], 0, kb[p], kb[p + 1], S::KV8);
+            }
+          }
+        }
+        if (!S::WIDE && S::QT > 1) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
+      }
+      // ---- online softmax over the tile
+      const int pos = tile_pos(w.s, i);
+      const bool whole = pos + kTile <= w.s.n && (pos >= w.s.lo || pos + kTile <= a.sinks);
+      constexpr int NR = S::WIDE ? 2 : 1;
+      uint32_t pt[NR][S::PT][2];
+      bool grow = false;
+      float fall[2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float top = m[r];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& v = s[nt][2 * r + c];
+            if (!whole && !visible(a, w.s, pos + 8 * nt + 2 * t + c)) v = -INFINITY;
+            top = fmaxf(top, v * rs[r]);
+          }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float base = top == -INFINITY ? 0.f : top;
+        fall[r] = ex2(m[r] - base);
+        grow = grow || top != m[r];
+        m[r] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          // (the exponent is rounded once, near 0 where it counts)
+          float p0 = ex2(fmaf(s[nt][2 * r], rs[r], S::SHIFT - base)), p1 = ex2(fmaf(s[nt][2 * r + 1], rs[r], S::SHIFT - base));
+          sum += p0 + p1;
+#pragma unroll
+          for (int k = 0; k < S::PT; ++k) pt[r][k][nt] = term<S::KV8>(p0, p1);
+        }
+        l[r] = l[r] * fall[r] + sum;
+      }
+      if (__any_sync(~0u, grow)) {
+#pragma unroll
+        for (int i2 = 0; i2 < D / 8; ++i2) {
+          o[i2][0] *= fall[0], o[i2][1] *= fall[0];
+          o[i2][2] *= fall[NR - 1], o[i2][3] *= fall[NR - 1];
+        }
+      }
+      // ---- o += p v
+      auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
+        if (S::WIDE) {
+#pragma unroll
+          for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][0], pt[NR - 1][k][0], pt[0][k][1], pt[NR - 1][k][1], b0, b1, S::KV8);
+        } else {
+          mma(c, pt[0][0][0], pt[0][1][0], pt[0][0][1], pt[0][1][1], b0, b1, S::KV8);
+          if (S::PT > 2) mma(c, pt[0][S::PT - 1][0], 0, pt[0][S::PT - 1][1], 0, b0, b1, S::KV8);
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < S::VC; ++c) {
+        uint32_t v[4][S::VB / 4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint8_t* p = at + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB;
+          if (S::VB == 16) {
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            v[r][0] = u.x, v[r][1] = u.y, v[r][S::VB / 4 - 2] = u.z, v[r][S::VB / 4 - 1] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            v[r][0] = u.x, v[r][1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < S::VB / 4; ++i2) {
+          if (S::KV8) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              // codes of two positions side by side, two dims in a register
+              const uint32_t e = __byte_perm(v[0][i2], v[1][i2], half ? 0x7362 : 0x5140);
+              const uint32_t d = __byte_perm(v[2][i2], v[3][i2], half ? 0x7362 : 0x5140);
+              pv(o[i2 * 4 + half * 2], widen(e), widen(d));
+              pv(o[i2 * 4 + half * 2 + 1], widen(e >> 16), widen(d >> 16));
+            }
+          } else {
+            pv(o[c * 8 + i2 * 2], __byte_perm(v[0][i2], v[1][i2], 0x5410), __byte_perm(v[2][i2], v[3][i2], 0x5410));
+            pv(o[c * 8 + i2 * 2 + 1], __byte_perm(v[0][i2], v[1][i2], 0x7632), __byte_perm(v[2][i2], v[3][i2], 0x7632));
+          }
+        }
+      }
+      bad = bad || (bad_stages >> stage & 1);
+      fetch(stage);
+      stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+    }
+
+    // ---- the warps' results joined
+    const int active = min(w.end - w.i, kWarps);
+#pragma unroll
+    for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (bad) l[r] = __int_as_float(0x7fffffff);
+      if (t == 0 && warp < active) {
+        merge_m[warp * S::ROWS + g + 8 * r] = m[r];
+        merge_l[warp * S::ROWS + g + 8 * r] = l[r];
+      }
+    }
+    __syncthreads();
+    if (warp < active) {
+#pragma unroll
+      for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
+        const int head = g + 8 * r;
+        if (head >= group) continue;
+        float top = -INFINITY;
+        for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[k * S::ROWS + head]);
+        const float e = top == -INFINITY ? 0.f : ex2(m[r] - top);
+        // a lane's accumulators are 2 runs of consecutive dims for each V chunk
+        constexpr int RUN = S::VB / S::E;
+        float* row = merge + (warp * S::ROWS + head) * D;
+#pragma unroll
+        for (int c = 0; c < S::VC; ++c)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < RUN; i += 4) {
+              float v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float* acc = o[c * RUN + i + k];
+                v[k] = (S::WIDE ? acc[2 * r + half] : acc[half] + acc[2 + half]) * e;
+              }
+              *reinterpret_cast<float4*>(row + c * 8 * RUN + (2 * t + half) * RUN + i) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+      }
+    }
+    __syncthreads();
+    const bool begins = w.i == 0, ends = w.end == w.s.tiles;
+    float* slot = args.parts + (blockIdx.x * 2ll + begins) * S::SLOT;
+    for (int i = threadIdx.x * 4; i < group * D; i += kThreads * 4) {
+      const int head = i / D, d = i % D;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float top = -INFINITY, den = 0.f;
+      for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[k * S::ROWS + head]);
+      for (int k = 0; k < active; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(merge + (k * S::ROWS + head) * D + d);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        den += merge_l[k * S::ROWS + head] * (top == -INFINITY ? 0.f : ex2(merge_m[k * S::ROWS + head] - top));
+      }
+      if (begins && ends) {
+        const float f = den == 0 ? 0.f : (S::KV8 ? a.v_scale : 1.f) / den;
+        store_out<S::IO32>(a.out_dev, w.b * a.out_seq_stride + (w.h * group + head) * a.out_head_stride + d,
+                           make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+        if (d == 0 && a.lse_dev)
+          a.lse_dev[static_cast<long long>(w.b) * a.n_q_heads + w.h * group + head] = lse_of(top, den, S::SHIFT);
+      } else {
+        *reinterpret_cast<float4*>(slot + head * D + d) = sum;
+        if (d == 0) slot[S::ROWS * D + head] = top, slot[S::ROWS * (D + 1) + head] = den;
+      }
+    }
+    if (begins && !ends && threadIdx.x == 0) {
+      // the CTA that holds the segment's last tile: the largest c with c * total / ctas <= it
+      const long long last = x + w.s.tiles - 1;
+      args.joins[blockIdx.x] = make_int4(w.b, w.h, static_cast<int>(((last + 1) * ctas - 1) / tiles_in_all), 0);
+    }
+    x += w.end - w.i;
+    if (w.left == 0) break;
+    walk_next(a, w);
+  }
+}
+
+// One CTA per (CTA that begins a segment which another ends, query head of the group):
+// the pieces of the segment joined by their maxima.
+template <class S>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args args) {
+  constexpr int D = S::D, TEAMS = kThreads / D;
+  __shared__ float factor[kMaxCtas], sums[TEAMS][D], red[2 * kWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const xlpk_attention_args& a = args.a;
+  const int4 j = args.joins[blockIdx.x];
+  if (j.x < 0) return;
+  const int head = blockIdx.y, group = a.n_q_heads / a.n_kv_heads, n = j.z - blockIdx.x + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // piece 0 is the slot of the segment that its CTA begins, the others continue theirs
+  auto slot = [&](int k) { return args.parts + ((blockIdx.x + k) * 2ll + (k == 0)) * S::SLOT; };
+  float top = -INFINITY;
+  for (int k = threadIdx.x; k < n; k += kThreads) top = fmaxf(top, factor[k] = slot(k)[S::ROWS * D + head]);
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, red[k]);
+  float den = 0.f;
+  for (int k = threadIdx.x; k < n; k += kThreads) {
+    const float e = top == -INFINITY ? 0.f : ex2(factor[k] - top);
+    factor[k] = e;
+    den += e * slot(k)[S::ROWS * (D + 1) + head];
+  }
+  for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(~0u, den, o);
+  if (lane == 0) red[kWarps + warp] = den;
+  __syncthreads();
+  den = 0.f;
+  for (int k = 0; k < kWarps; ++k) den += red[kWarps + k];
+  const int d = threadIdx.x % D, team = threadIdx.x / D;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int k = team; k < n; k += TEAMS) sum += factor[k] * slot(k)[head * D + d];
+  sums[team][d] = sum;
+  __syncthreads();
+  if (team != 0) return;
+  for (int k = 1; k < TEAMS; ++k) sum += sums[k][d];
+  const float v = den == 0 ? 0.f : sum * (S::KV8 ? a.v_scale : 1.f) / den;
+  const long long at = j.x * a.out_seq_stride + (j.y * group + head) * a.out_head_stride + d;
+  if (S::IO32)
+    static_cast<float*>(a.out_dev)[at] = v;
+  else
+    static_cast<__nv_bfloat16*>(a.out_dev)[at] = __float2bfloat16_rn(v);
+  if (d == 0 && a.lse_dev) a.lse_dev[static_cast<long long>(j.x) * a.n_q_heads + j.y * group + head] = lse_of(top, den, S::SHIFT);
 }
 
 bool power_of_two_scale(float s) {
@@ -170,9 +731,46 @@ xlpk_status check_args(const xlpk_attention_args* a) {
   return XLPK_OK;
 }
 
+template <class S>
+xlpk_status launch(const Args& args, int ctas, cudaStream_t st) {
+  static std::atomic<unsigned long long> ready;   // devices whose kernel has its shared memory
+  int dev = 0;
+  XLPK_CUDA(cudaGetDevice(&dev));
+  if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    XLPK_CUDA(cudaFuncSetAttribute(attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  attention_kernel<S><<<ctas, kThreads, S::SMEM, st>>>(args);
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(ctas, args.a.n_q_heads / args.a.n_kv_heads);
+  c.blockDim = dim3(kThreads);
+  c.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  XLPK_CUDA(cudaLaunchKernelEx(&c, join_kernel<S>, args));
+  return XLPK_OK;
+}
+
+template <int D, bool KV8>
+xlpk_status launch_for(const Args& args, int ctas, cudaStream_t st) {
+  const bool io32 = args.a.io_dtype == XLPK_DTYPE_FP32;
+  if (args.a.n_q_heads / args.a.n_kv_heads > 8)
+    return io32 ? launch<Shape<D, KV8, true, true>>(args, ctas, st) : launch<Shape<D, KV8, true, false>>(args, ctas, st);
+  return io32 ? launch<Shape<D, KV8, false, true>>(args, ctas, st) : launch<Shape<D, KV8, false, false>>(args, ctas, st);
+}
+
+constexpr int64_t kJoinBytes = kMaxCtas * sizeof(int4);
+
 }  // namespace
 
-extern "C" int64_t xlpk_decode_attention_workspace(const xlpk_attention_args* a) { return shape_ok(a) ? 16 : 0; }
+extern "C" int64_t xlpk_decode_attention_workspace(const xlpk_attention_args* a) {
+  if (!shape_ok(a)) return 0;
+  const int64_t rows = a->n_q_heads / a->n_kv_heads > 8 ? 16 : 8;
+  return kJoinBytes + kMaxCtas * 2 * rows * (static_cast<int64_t>(a->head_dim) + 2) * 4;
+}
 
 extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void* workspace_dev, int64_t workspace_bytes,
                                              void* stream) {
@@ -184,8 +782,13 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   const xlpk_status dev = current_sms(&sms);
   if (dev != XLPK_OK) return dev;
   if (a->n_seqs == 0) return XLPK_OK;
-  if (a->n_seqs > 65535) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: more than 65535 sequences");
-  attention_kernel<<<dim3(a->n_q_heads, a->n_seqs), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  XLPK_CUDA(cudaGetLastError());
-  return XLPK_OK;
+  Args args;
+  args.a = *a;
+  args.joins = static_cast<int4*>(workspace_dev);
+  args.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + kJoinBytes);
+  const int ctas = std::min(sms, kMaxCtas);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a->head_dim == 64)
+    return a->kv_dtype == XLPK_DTYPE_BF16 ? launch_for<64, false>(args, ctas, st) : launch_for<64, true>(args, ctas, st);
+  return a->kv_dtype == XLPK_DTYPE_BF16 ? launch_for<128, false>(args, ctas, st) : launch_for<128, true>(args, ctas, st);
 }
