@@ -92,7 +92,8 @@ class xlpk_page_pool(C.Structure):
                                               "cols")]
 
 
-# name -> (restype, argtypes); every symbol the header declares
+# name -> (restype, argtypes); every symbol the header declares.  Structs of the stand-alone
+# operators are passed by address (c_void_p), so that packed bytes serve as well.
 SIGNATURES = {
     "xlpk_create": (C.c_int32, [C.POINTER(xlpk_config), C.POINTER(xlpk_weights),
                                 C.POINTER(xlpk_kv), C.POINTER(C.c_void_p)]),
@@ -117,14 +118,14 @@ SIGNATURES = {
     "xlpk_status_string": (C.c_char_p, [C.c_int32]),
     "xlpk_last_cuda_error": (C.c_char_p, []),
     "xlpk_tc_gemm_tile": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p]),
-    "xlpk_decode_attention_workspace": (C.c_int64, [C.POINTER(xlpk_attention_args)]),
-    "xlpk_decode_attention": (C.c_int32, [C.POINTER(xlpk_attention_args), C.c_void_p, C.c_int64, C.c_void_p]),
-    "xlpk_pages_workspace": (C.c_int64, [C.POINTER(xlpk_page_pool)]),
-    "xlpk_pages_fork": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
-    "xlpk_pages_reserve": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p]),
-    "xlpk_pages_trim": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_int32, C.c_int32, C.c_void_p]),
-    "xlpk_pages_compact": (C.c_int32, [C.POINTER(xlpk_page_pool), C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
-    "xlpk_pages_copy": (C.c_int32, [C.POINTER(xlpk_page_pool), C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
+    "xlpk_decode_attention_workspace": (C.c_int64, [C.c_void_p]),
+    "xlpk_decode_attention": (C.c_int32, [C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_workspace": (C.c_int64, [C.c_void_p]),
+    "xlpk_pages_fork": (C.c_int32, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_reserve": (C.c_int32, [C.c_void_p, C.c_void_p, C.c_void_p]),
+    "xlpk_pages_trim": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int32, C.c_void_p]),
+    "xlpk_pages_compact": (C.c_int32, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "xlpk_pages_copy": (C.c_int32, [C.c_void_p, C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
                                     C.c_void_p]),
     "xlpk_token_logprobs": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_int64, C.c_void_p, C.c_int32,
                                         C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),

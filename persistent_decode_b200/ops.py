@@ -9,38 +9,57 @@ torch's allocator on that stream, one for each call, so calls on several streams
 and captured CUDA graphs do not share any.  Wrong dtypes, shapes and devices
 raise ValueError, refused calls XlpkError; what only the device can see goes to
 a status word.  No gradients are recorded.
+
+The smallest calls take a few microseconds on the GPU, so the host side is kept
+short: messages are only put together for a call that fails, arguments are
+packed in one go, and nothing is asked of the library twice.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
-import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _abi
-from .engine import XlpkError, _check, _ptr, lib
+from .engine import XlpkError, _check, get_lib
 
 _IO = {torch.float32: _abi.XLPK_DTYPE_FP32, torch.bfloat16: _abi.XLPK_DTYPE_BF16}
 _KV = {torch.bfloat16: _abi.XLPK_DTYPE_BF16, torch.uint8: _abi.XLPK_DTYPE_FP8_E4M3,
        torch.float8_e4m3fn: _abi.XLPK_DTYPE_FP8_E4M3}
+_I32 = (torch.int32,)
+_ATTENTION = struct.Struct("10P15q11i3f")    # xlpk_attention_args
+_POOL = struct.Struct("6P7i4x")              # xlpk_page_pool
+_F = {}                                      # the library's functions
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _fn(name: str):
+    f = _F.get(name)
+    if f is None:
+        f = _F[name] = getattr(get_lib(), name)
+    return f
 
 
-def _tensor(t, name: str, dim: int, dtypes, device) -> None:
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(device is None or t.device == device, f"{name} is on {t.device}, not on {device}")
-    _need(t.dim() == dim and t.dtype in dtypes, f"{name}: {t.dim()}-d {t.dtype}, want {dim}-d {' or '.join(map(str, dtypes))}")
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _steps(t):
-    """Strides of all but the last dimension (0 where there is nothing to step to)."""
-    return [s if n > 1 else 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+def _tensor(t, name: str, dim: int, dtypes, device: int) -> None:
+    """`t` is a `dim`-d CUDA tensor of one of `dtypes`, on GPU `device` (< 0: any)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == dim:
+        at = t.get_device()
+        if at >= 0 and (at == device or device < 0):
+            return
+    have = f"{t.dim()}-d {t.dtype} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+    where = "a GPU" if device < 0 else f"cuda:{device}"
+    _refuse(f"{name} is {have}, want {dim}-d {' or '.join(str(d) for d in dtypes)} on {where}")
+
+
+def _int32(v, name: str) -> int:
+    if not -(1 << 31) <= v < 1 << 31:
+        _refuse(f"{name} = {v} does not fit an int32")
+    return int(v)
 
 
 def _distinct(t) -> bool:
@@ -53,22 +72,43 @@ def _distinct(t) -> bool:
     return True
 
 
-@contextlib.contextmanager
-def _on(device, stream, tensors=()):
-    """The stream handle to launch on; allocations inside belong to that stream."""
-    if stream is None:
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream or None
-        return
-    _need(stream.device == device, f"stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.stream(stream):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)   # their memory is not reused before this use of it
-        yield stream.cuda_stream or None
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+class _On:
+    """The stream a call launches on: its allocations belong to it, and so, for an
+    explicit stream, do the tensors it uses, until that use is over."""
+    __slots__ = ("scope", "handle")
+
+    def __init__(self, device: int, stream, tensors):
+        if stream is None:
+            self.scope = None if torch.cuda.current_device() == device else torch.cuda.device(device)
+        else:
+            if stream.device.index != device:
+                _refuse(f"stream is on {stream.device}, the tensors on cuda:{device}")
+            self.scope = torch.cuda.stream(stream)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+            self.handle = stream.cuda_stream
+        if stream is None:
+            self.handle = torch._C._cuda_getCurrentRawStream(device)
+
+    def __enter__(self):
+        if self.scope is not None:
+            self.scope.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.scope is not None:
+            self.scope.__exit__(*exc)
 
 
 # ---- attention
+
+_WORKSPACE = {}    # (wide group, head_dim) -> bytes
+
 
 def decode_attention(q, k_cache, v_cache, seq_lens, page_table=None, *, k_new=None, v_new=None,
                      scale: Optional[float] = None, window: int = 0, sinks: int = 0, k_scale: float = 1.0,
@@ -89,59 +129,76 @@ def decode_attention(q, k_cache, v_cache, seq_lens, page_table=None, *, k_new=No
     visible position names a page outside the pool or a length does not fit
     (that sequence's output is NaN).
     """
-    _tensor(q, "q", 3, _IO, None)
-    dev = q.device
-    B, H, D = q.shape
+    _tensor(q, "q", 3, _IO, -1)
+    dev = q.get_device()
     _tensor(k_cache, "k_cache", 4, _KV, dev)
     _tensor(v_cache, "v_cache", 4, (k_cache.dtype,), dev)
-    n_pages, KH, P, dc = k_cache.shape
-    _need(v_cache.shape == k_cache.shape and dc == D, f"caches of {tuple(k_cache.shape)} and {tuple(v_cache.shape)} for head_dim {D}")
-    _tensor(seq_lens, "seq_lens", 1, (torch.int32,), dev)
-    _need(seq_lens.shape[0] == B and (B < 2 or seq_lens.stride(0) == 1), "seq_lens must be a contiguous [B]")
-    _need(D > 0 and all(t.stride(-1) == 1 for t in (q, k_cache, v_cache)), "rows of head_dim must be contiguous")
-    a = _abi.xlpk_attention_args()
-    if page_table is not None:
-        _tensor(page_table, "page_table", 2, (torch.int32,), dev)
-        _need(page_table.shape[0] == B and (page_table.shape[1] < 2 or page_table.stride(1) == 1),
-              "page_table must be [B][pages] with contiguous rows")
-        a.page_table_dev, a.table_cols = _ptr(page_table), page_table.shape[1]
-        a.table_stride = page_table.stride(0) if B > 1 else 0
+    _tensor(seq_lens, "seq_lens", 1, _I32, dev)
+    B, H, D = q.shape
+    n_pages, KH, P, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or d != D or D == 0:
+        _refuse(f"caches of {tuple(k_cache.shape)} and {tuple(v_cache.shape)} for head_dim {D}")
+    if seq_lens.shape[0] != B or (B > 1 and seq_lens.stride(0) != 1):
+        _refuse("seq_lens must be a contiguous [B]")
+    qs, ks, vs = q.stride(), k_cache.stride(), v_cache.stride()
+    if qs[2] != 1 or ks[3] != 1 or vs[3] != 1:
+        _refuse("rows of head_dim must be contiguous")
+    # nothing steps along a dimension of one element: its stride is not looked at
+    one_b, one_h, one_kh, one_p, one_pos = B < 2, H < 2, KH < 2, n_pages < 2, P < 2
+    if page_table is None:
+        if n_pages != B:
+            _refuse(f"a contiguous cache of {n_pages} sequences for {B} queries")
+        table_at, cols, table_step = 0, 1, 0
     else:
-        _need(n_pages == B, f"a contiguous cache of {n_pages} sequences for {B} queries")
-        a.table_cols = 1
-    _need((k_new is None) == (v_new is None), "k_new and v_new come together")
-    if k_new is not None:
+        _tensor(page_table, "page_table", 2, _I32, dev)
+        rows, cols = page_table.shape
+        if rows != B or (cols > 1 and page_table.stride(1) != 1):
+            _refuse("page_table must be [B][pages] with contiguous rows")
+        table_at, table_step = page_table.data_ptr(), 0 if one_b else page_table.stride(0)
+    kn = vn = nk0 = nk1 = nv0 = nv1 = 0
+    if k_new is not None or v_new is not None:
         for t, name in ((k_new, "k_new"), (v_new, "v_new")):
             _tensor(t, name, 3, (q.dtype,), dev)
-            _need(t.shape == (B, KH, D) and t.stride(-1) == 1, f"{name} must be [B][n_kv][d] with contiguous rows")
-        _need(_distinct(k_cache) and _distinct(v_cache), "a cache that is written must not overlap itself")
-        a.k_new_dev, a.v_new_dev = _ptr(k_new), _ptr(v_new)
-        a.new_k_seq_stride, a.new_k_head_stride = _steps(k_new)
-        a.new_v_seq_stride, a.new_v_head_stride = _steps(v_new)
+            if t.shape != (B, KH, D) or t.stride(2) != 1:
+                _refuse(f"{name} must be [B][n_kv][d] with contiguous rows")
+        if not (k_cache.is_contiguous() or _distinct(k_cache)) or not (v_cache.is_contiguous() or _distinct(v_cache)):
+            _refuse("a cache that is written must not overlap itself")
+        kn, vn = k_new.data_ptr(), v_new.data_ptr()
+        (nk0, nk1, _), (nv0, nv1, _) = k_new.stride(), v_new.stride()
     if out is not None:
         _tensor(out, "out", 3, (q.dtype,), dev)
-        _need(out.shape == q.shape and out.stride(-1) == 1 and _distinct(out), "out must be [B][n_q][d] with rows of its own")
+        if out.shape != q.shape or out.stride(2) != 1 or not _distinct(out):
+            _refuse("out must be [B][n_q][d] with rows of its own")
     if status is not None:
-        _tensor(status, "status", 1, (torch.int32,), dev)
-        _need(status.shape[0] >= 1, "status must hold one int32")
-    a.q_dev, a.k_dev, a.v_dev, a.seq_lens_dev, a.status_dev = (_ptr(t) for t in (q, k_cache, v_cache, seq_lens, status))
-    a.q_seq_stride, a.q_head_stride = _steps(q)
-    a.k_page_stride, a.k_head_stride, a.k_pos_stride = _steps(k_cache)
-    a.v_page_stride, a.v_head_stride, a.v_pos_stride = _steps(v_cache)
-    a.n_seqs, a.n_q_heads, a.n_kv_heads, a.head_dim, a.n_pages, a.page_size = B, H, KH, D, n_pages, P
-    a.io_dtype, a.kv_dtype = _IO[q.dtype], _KV[k_cache.dtype]
-    a.window, a.sinks, a.k_scale, a.v_scale = int(window), int(sinks), float(k_scale), float(v_scale)
-    a.scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    with _on(dev, stream, (q, k_cache, v_cache, seq_lens, page_table, k_new, v_new, out, status)) as handle:
+        _tensor(status, "status", 1, _I32, dev)
+        if status.shape[0] < 1:
+            _refuse("status must hold one int32")
+    with _On(dev, stream, (q, k_cache, v_cache, seq_lens, page_table, k_new, v_new, out, status)) as handle:
         if out is None:
-            out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
-        a.out_dev = _ptr(out)
-        a.out_seq_stride, a.out_head_stride = _steps(out)
-        lse = torch.empty((B, H), dtype=torch.float32, device=dev) if return_lse else None
-        a.lse_dev = _ptr(lse)
-        n = lib.xlpk_decode_attention_workspace(C.byref(a))
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-        _check(lib.xlpk_decode_attention(C.byref(a), _ptr(ws), ws.numel(), handle), "xlpk_decode_attention")
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = q.new_empty((B, H), dtype=torch.float32) if return_lse else None
+        os = out.stride()
+        args = _ATTENTION.pack(
+            q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), table_at, seq_lens.data_ptr(), out.data_ptr(),
+            _ptr(lse), _ptr(status),
+            0 if one_b else qs[0], 0 if one_h else qs[1],
+            0 if one_b else nk0, 0 if one_kh else nk1, 0 if one_b else nv0, 0 if one_kh else nv1,
+            0 if one_b else os[0], 0 if one_h else os[1],
+            0 if one_p else ks[0], 0 if one_kh else ks[1], 0 if one_pos else ks[2],
+            0 if one_p else vs[0], 0 if one_kh else vs[1], 0 if one_pos else vs[2], table_step,
+            B, H, KH, D, n_pages, P, cols, _IO[q.dtype], _KV[k_cache.dtype],
+            _int32(window, "window"), _int32(sinks, "sinks"),
+            D ** -0.5 if scale is None else scale, k_scale, v_scale)
+        key = (KH > 0 and H > 8 * KH, D)
+        need = _WORKSPACE.get(key)
+        if need is None:
+            need = _fn("xlpk_decode_attention_workspace")(args)
+            if need:
+                _WORKSPACE[key] = need
+        ws = q.new_empty((max(need, 16),), dtype=torch.uint8)
+        st = _fn("xlpk_decode_attention")(args, ws.data_ptr(), need, handle)
+        if st:
+            _check(st, "xlpk_decode_attention")
     return (out, lse) if return_lse else out
 
 
@@ -159,68 +216,86 @@ class PagePool:
     """
 
     def __init__(self, k, v, page_table, seq_lens, refs=None, status=None):
-        _tensor(k, "k", 5, _KV, None)
-        dev = self.device = k.device
+        _tensor(k, "k", 5, _KV, -1)
+        dev = k.get_device()
         _tensor(v, "v", 5, (k.dtype,), dev)
-        _tensor(page_table, "page_table", 2, (torch.int32,), dev)
-        _tensor(seq_lens, "seq_lens", 1, (torch.int32,), dev)
+        _tensor(page_table, "page_table", 2, _I32, dev)
+        _tensor(seq_lens, "seq_lens", 1, _I32, dev)
         L, n_pages, KH, P, D = k.shape
         if refs is None:
             held = page_table.reshape(-1)
             held = held[(held >= 0) & (held < n_pages)]
             refs = torch.bincount(held, minlength=n_pages).to(torch.int32)
         if status is None:
-            status = torch.zeros(1, dtype=torch.int32, device=dev)
-        _tensor(refs, "refs", 1, (torch.int32,), dev)
-        _tensor(status, "status", 1, (torch.int32,), dev)
+            status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        _tensor(refs, "refs", 1, _I32, dev)
+        _tensor(status, "status", 1, _I32, dev)
         rows, cols = page_table.shape
-        _need(v.shape == k.shape, f"pools of {tuple(k.shape)} and {tuple(v.shape)}")
-        _need(seq_lens.shape[0] == rows and refs.shape[0] == n_pages and status.shape[0] >= 1,
-              "seq_lens must have the table's rows, refs the pool's pages")
-        _need(all(t.is_contiguous() for t in (k, v, page_table, seq_lens, refs)), "pool tensors must be contiguous")
+        if v.shape != k.shape:
+            _refuse(f"pools of {tuple(k.shape)} and {tuple(v.shape)}")
+        if seq_lens.shape[0] != rows or refs.shape[0] != n_pages or status.shape[0] < 1:
+            _refuse("seq_lens must have the table's rows, refs the pool's pages")
+        if not (k.is_contiguous() and v.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
+                and refs.is_contiguous()):
+            _refuse("pool tensors must be contiguous")
         self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status = k, v, page_table, seq_lens, refs, status
-        self._c = _abi.xlpk_page_pool(_ptr(k), _ptr(v), _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(status),
-                                      L, n_pages, KH, P, D * k.element_size(), rows, cols)
+        self._device, self._rows_n = dev, rows
+        self._c = _POOL.pack(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
+                             status.data_ptr(), L, n_pages, KH, P, D * k.element_size(), rows, cols)
 
-    def _call(self, name, stream, *args, workspace: bool = False, uses=()):
-        with _on(self.device, stream, (self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status, *uses)) as handle:
-            if workspace:
-                n = lib.xlpk_pages_workspace(C.byref(self._c))
-                ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
-                args = (*args, _ptr(ws), ws.numel())
-            _check(getattr(lib, name)(C.byref(self._c), *args, handle), name)
+    @property
+    def device(self):
+        return self.k.device
 
-    def _rows(self, t, name: str):
-        _tensor(t, name, 1, (torch.int32,), self.device)
-        _need(t.shape[0] == self.page_table.shape[0] and t.is_contiguous(), f"{name} must be a contiguous [rows]")
-        return _ptr(t)
+    def _uses(self, *more):
+        return (self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status, *more)
+
+    def _workspace(self):
+        n = _fn("xlpk_pages_workspace")(self._c)
+        return self.refs.new_empty((max(n, 16),), dtype=torch.uint8), n
+
+    def _per_row(self, t, name: str) -> int:
+        _tensor(t, name, 1, _I32, self._device)
+        if t.shape[0] != self._rows_n or not t.is_contiguous():
+            _refuse(f"{name} must be a contiguous [rows]")
+        return t.data_ptr()
 
     def fork(self, parents, stream=None) -> None:
         """xlpk_pages_fork: row r becomes what row parents[r] was (-1: empty); `parents` int32 [rows]."""
-        self._call("xlpk_pages_fork", stream, self._rows(parents, "parents"), workspace=True, uses=(parents,))
+        at = self._per_row(parents, "parents")
+        with _On(self._device, stream, self._uses(parents)) as handle:
+            ws, n = self._workspace()
+            _check(_fn("xlpk_pages_fork")(self._c, at, ws.data_ptr(), n, handle), "xlpk_pages_fork")
 
     def reserve(self, want, stream=None) -> None:
         """xlpk_pages_reserve: pages so that row r can hold want[r] positions; `want` int32 [rows]."""
-        self._call("xlpk_pages_reserve", stream, self._rows(want, "want"), uses=(want,))
+        at = self._per_row(want, "want")
+        with _On(self._device, stream, self._uses(want)) as handle:
+            _check(_fn("xlpk_pages_reserve")(self._c, at, handle), "xlpk_pages_reserve")
 
     def trim(self, window: int, sinks: int = 0, stream=None) -> None:
         """xlpk_pages_trim: give back the pages a sliding window has passed."""
-        self._call("xlpk_pages_trim", stream, int(window), int(sinks))
+        with _On(self._device, stream, self._uses()) as handle:
+            _check(_fn("xlpk_pages_trim")(self._c, _int32(window, "window"), _int32(sinks, "sinks"), handle), "xlpk_pages_trim")
 
     def compact(self, stream=None):
         """xlpk_pages_compact: move the live pages to the lowest numbers; returns the new
         number of every page, int32 [n_pages] (-1: free)."""
-        with _on(self.device, stream):
-            remap = torch.empty(self.refs.shape[0], dtype=torch.int32, device=self.device)
-        self._call("xlpk_pages_compact", stream, _ptr(remap), workspace=True)
+        with _On(self._device, stream, self._uses()) as handle:
+            remap = torch.empty_like(self.refs)
+            ws, n = self._workspace()
+            _check(_fn("xlpk_pages_compact")(self._c, remap.data_ptr(), ws.data_ptr(), n, handle), "xlpk_pages_compact")
         return remap
 
     def copy(self, src, dst, stream=None) -> None:
         """xlpk_pages_copy: page src[i] to page dst[i] in every layer (host integers)."""
-        src, dst = [int(p) for p in src], [int(p) for p in dst]
-        _need(len(src) == len(dst), "src and dst of different lengths")
+        src, dst = [_int32(p, "a page") for p in src], [_int32(p, "a page") for p in dst]
         n = len(src)
-        self._call("xlpk_pages_copy", stream, (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n)
+        if len(dst) != n:
+            _refuse("src and dst of different lengths")
+        with _On(self._device, stream, self._uses()) as handle:
+            _check(_fn("xlpk_pages_copy")(self._c, (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n, handle),
+                   "xlpk_pages_copy")
 
     def check(self) -> None:
         """Waits for the calls so far; raises what stopped one of them, and lets the pool go on."""
@@ -247,24 +322,31 @@ def token_logprobs(logits, tokens, top_k: int = 0, stream=None) -> TokenLogprobs
     rows at any stride; `tokens` int32 of the leading shape.  top_k <= 64
     alternatives, best first, ties by the lower id.  Masked logits are -inf.
     """
-    _need(isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() >= 1 and logits.dtype in _IO,
-          "logits must be an fp32 or bf16 CUDA tensor [..., vocab]")
-    dev, vocab = logits.device, logits.shape[-1]
-    _tensor(tokens, "tokens", logits.dim() - 1, (torch.int32,), dev)
-    _need(tokens.shape == logits.shape[:-1] and tokens.is_contiguous(), "tokens must be contiguous, one for each row of logits")
-    _need(vocab > 0 and (vocab == 1 or logits.stride(-1) == 1), "rows of logits must be contiguous")
-    rows = tokens.numel()
-    try:
-        x = logits if logits.dim() == 2 else logits.view(rows, vocab)
-    except RuntimeError:
-        raise ValueError("the leading dimensions of logits must step evenly") from None
-    shape = tuple(tokens.shape)
-    with _on(dev, stream, (logits, tokens)) as handle:
-        f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
-        logprob, entropy, rank = torch.empty(shape, **f32), torch.empty(shape, **f32), torch.empty(shape, **i32)
-        top_ids = torch.empty((*shape, top_k), **i32) if top_k > 0 else None
-        top = torch.empty((*shape, top_k), **f32) if top_k > 0 else None
-        _check(lib.xlpk_token_logprobs(_ptr(x), _IO[x.dtype], rows, vocab, x.stride(0) if rows > 1 else 0, _ptr(tokens),
-                                       int(top_k), _ptr(logprob), _ptr(entropy), _ptr(rank), _ptr(top_ids), _ptr(top),
-                                       handle), "xlpk_token_logprobs")
+    if not isinstance(logits, torch.Tensor) or logits.dim() < 1 or logits.dtype not in _IO or not logits.is_cuda:
+        _refuse("logits must be an fp32 or bf16 CUDA tensor [..., vocab]")
+    dev, vocab, dims = logits.get_device(), logits.shape[-1], logits.dim()
+    _tensor(tokens, "tokens", dims - 1, _I32, dev)
+    if tokens.shape != logits.shape[:-1] or not tokens.is_contiguous():
+        _refuse("tokens must be contiguous, one for each row of logits")
+    if vocab == 0 or (vocab > 1 and logits.stride(-1) != 1):
+        _refuse("rows of logits must be contiguous")
+    rows, top_k = tokens.numel(), _int32(top_k, "top_k")
+    x = logits
+    if dims != 2:
+        try:
+            x = logits.view(rows, vocab)
+        except RuntimeError:
+            _refuse("the leading dimensions of logits must step evenly")
+    with _On(dev, stream, (logits, tokens)) as handle:
+        rank = torch.empty_like(tokens)
+        logprob, entropy = tokens.new_empty((2, *tokens.shape), dtype=torch.float32).unbind(0)
+        top_ids = top = None
+        if top_k > 0:
+            top_ids = tokens.new_empty((*tokens.shape, top_k))
+            top = tokens.new_empty((*tokens.shape, top_k), dtype=torch.float32)
+        st = _fn("xlpk_token_logprobs")(
+            x.data_ptr(), _IO[x.dtype], rows, vocab, x.stride(0) if rows > 1 else 0, tokens.data_ptr(), top_k,
+            logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), _ptr(top_ids), _ptr(top), handle)
+        if st:
+            _check(st, "xlpk_token_logprobs")
     return TokenLogprobs(logprob, entropy, rank, top_ids, top)
