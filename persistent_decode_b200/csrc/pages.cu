@@ -21,6 +21,9 @@ namespace {
 constexpr int kMaxRows = 1024;
 constexpr int kPlanThreads = 1024;   // one thread per table row
 constexpr int kCopyThreads = 256;
+constexpr int kCopyCtas = 8;         // per SM
+constexpr int kCopyUnroll = 4;
+constexpr int kSegment = kCopyThreads * kCopyUnroll * 16;   // bytes a CTA copies at a time
 constexpr int kTableCols = 8;        // columns of one table block of the fork
 constexpr int kListPairs = 480;      // page pairs in one launch's parameters
 
@@ -92,6 +95,7 @@ __host__ __device__ inline ForkPlan fork_plan_at(void* ws, int rows) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const xlpk_page_pool p, const int* parents, void* ws) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int heir[kMaxRows], children[kMaxRows], lens[kMaxRows], list[2 * kPlanThreads], warp_sums[32];
   const ForkPlan f = fork_plan_at(ws, p.rows);
   const int r = threadIdx.x;
@@ -147,15 +151,29 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const xlpk_page
   if (r == 0) *f.count = copies;
 }
 
-// n runs of `bytes` (a multiple of 16), run i of CTA-strided order
-__device__ inline void copy_run(uint8_t* dst, const uint8_t* src, long long bytes) {
-  for (long long i = threadIdx.x * 16ll; i < bytes; i += kCopyThreads * 16ll)
-    *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(src + i);
+// Copies bytes [at, at + kSegment) of a run: kCopyUnroll 16-byte loads of every thread are in flight before
+// the first store.  `bytes` is a multiple of 16.
+__device__ inline void copy_segment(uint8_t* dst, const uint8_t* src, long long at, long long bytes) {
+  uint4 v[kCopyUnroll];
+#pragma unroll
+  for (int i = 0; i < kCopyUnroll; ++i) {
+    const long long o = at + (threadIdx.x + i * kCopyThreads) * 16;
+    if (o < bytes)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                   : "l"(src + o));
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyUnroll; ++i) {
+    const long long o = at + (threadIdx.x + i * kCopyThreads) * 16;
+    if (o < bytes) *reinterpret_cast<uint4*>(dst + o) = v[i];
+  }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const xlpk_page_pool p, const int* parents, void* ws,
                                                                   int table_blocks) {
   extern __shared__ int tile[];   // [rows][kTableCols]
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan
   const ForkPlan f = fork_plan_at(ws, p.rows);
   const int copies = *f.count;
   if (copies < 0) return;
@@ -185,14 +203,13 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const xlpk_pag
     return;
   }
   const long long head = static_cast<long long>(p.page_size) * p.row_bytes, page = head * p.n_kv_heads;
-  const int per_copy = p.n_layers * 2 * p.n_kv_heads;
+  const int segs = static_cast<int>((head + kSegment - 1) / kSegment), per_copy = p.n_layers * 2 * p.n_kv_heads * segs;
   for (long long u = blockIdx.x - table_blocks; u < static_cast<long long>(copies) * per_copy; u += gridDim.x - table_blocks) {
-    const int k = static_cast<int>(u / per_copy), w = static_cast<int>(u % per_copy), h = w % p.n_kv_heads,
-              layer = w / p.n_kv_heads / 2;
-    uint8_t* pool = static_cast<uint8_t*>(w / p.n_kv_heads % 2 ? p.v_dev : p.k_dev);
-    const long long base = static_cast<long long>(layer) * p.n_pages * page + h * head;
-    copy_run(pool + base + f.dst[k] * page, pool + base + f.src[k] * page,
-             static_cast<long long>(f.filled[k]) * p.row_bytes);
+    const int k = static_cast<int>(u / per_copy), w = static_cast<int>(u % per_copy), seg = w % segs, h = w / segs % p.n_kv_heads,
+              plane = w / segs / p.n_kv_heads;   // K and V of each layer
+    uint8_t* pool = static_cast<uint8_t*>(plane & 1 ? p.v_dev : p.k_dev) + static_cast<long long>(plane >> 1) * p.n_pages * page + h * head;
+    copy_segment(pool + f.dst[k] * page, pool + f.src[k] * page, static_cast<long long>(seg) * kSegment,
+                 static_cast<long long>(f.filled[k]) * p.row_bytes);
   }
 }
 
@@ -275,6 +292,7 @@ __host__ __device__ inline CompactPlan compact_plan_at(void* ws, int n_pages) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const xlpk_page_pool p, int* remap_dev, void* ws) {
+  asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int warp_sums[32];
   const CompactPlan c = compact_plan_at(ws, p.n_pages);
   int* remap = remap_dev ? remap_dev : c.remap;
@@ -310,15 +328,18 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const xlpk_p
 
 __device__ inline void copy_pages(const xlpk_page_pool& p, int n, const int* src, const int* dst, int block, int blocks) {
   const long long page = static_cast<long long>(p.page_size) * p.row_bytes * p.n_kv_heads;
-  for (long long u = block; u < static_cast<long long>(n) * p.n_layers * 2; u += blocks) {
-    const int k = static_cast<int>(u / (p.n_layers * 2)), w = static_cast<int>(u % (p.n_layers * 2));
-    uint8_t* pool = static_cast<uint8_t*>(w & 1 ? p.v_dev : p.k_dev) + static_cast<long long>(w >> 1) * p.n_pages * page;
-    copy_run(pool + dst[k] * page, pool + src[k] * page, page);
+  const long long segs = (page + kSegment - 1) / kSegment, per_page = segs * p.n_layers * 2;
+  for (long long u = block; u < n * per_page; u += blocks) {
+    const int k = static_cast<int>(u / per_page);
+    const long long w = u - k * per_page, plane = w / segs;
+    uint8_t* pool = static_cast<uint8_t*>(plane & 1 ? p.v_dev : p.k_dev) + (plane >> 1) * p.n_pages * page;
+    copy_segment(pool + dst[k] * page, pool + src[k] * page, (w - plane * segs) * kSegment, page);
   }
 }
 
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const xlpk_page_pool p, const int* remap_dev,
                                                                      void* ws, int table_blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan
   const CompactPlan c = compact_plan_at(ws, p.n_pages);
   const int n = *c.count;
   if (n < 0) return;
@@ -364,6 +385,23 @@ xlpk_status check_pool(const xlpk_page_pool* p) {
   return XLPK_OK;
 }
 
+// A launch that may be set up while the one before it runs; the kernel waits for its end.
+template <class... K, class... A>
+xlpk_status launch_after(void (*kernel)(K...), int blocks, int smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(kCopyThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  XLPK_CUDA(cudaLaunchKernelEx(&c, kernel, static_cast<K>(args)...));
+  return XLPK_OK;
+}
+
 xlpk_status check_workspace(const xlpk_page_pool* p, const void* ws, int64_t bytes) {
   if (!ws || !aligned(ws, 16) || bytes < xlpk_pages_workspace(p))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_pages: workspace missing, unaligned or too small");
@@ -395,9 +433,8 @@ xlpk_status xlpk_pages_fork(const xlpk_page_pool* p, const int32_t* parents_dev,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(*p, parents_dev, ws);
   const int table_blocks = (p->cols + kTableCols - 1) / kTableCols;
-  fork_apply_kernel<<<table_blocks + sms * 4, kCopyThreads, p->rows * kTableCols * 4, st>>>(*p, parents_dev, ws, table_blocks);
-  XLPK_CUDA(cudaGetLastError());
-  return XLPK_OK;
+  return launch_after(fork_apply_kernel, table_blocks + sms * kCopyCtas, p->rows * kTableCols * 4, st, *p, parents_dev, ws,
+                      table_blocks);
 }
 
 xlpk_status xlpk_pages_reserve(const xlpk_page_pool* p, const int32_t* want_dev, void* stream) {
@@ -433,9 +470,7 @@ xlpk_status xlpk_pages_compact(const xlpk_page_pool* p, int32_t* remap_dev, void
   compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(*p, remap_dev, ws);
   const long long n = static_cast<long long>(p->rows) * p->cols;
   const int table_blocks = static_cast<int>(std::min<long long>(sms, (n + kCopyThreads - 1) / kCopyThreads));
-  compact_apply_kernel<<<table_blocks + sms * 4, kCopyThreads, 0, st>>>(*p, remap_dev, ws, table_blocks);
-  XLPK_CUDA(cudaGetLastError());
-  return XLPK_OK;
+  return launch_after(compact_apply_kernel, table_blocks + sms * kCopyCtas, 0, st, *p, remap_dev, ws, table_blocks);
 }
 
 xlpk_status xlpk_pages_copy(const xlpk_page_pool* p, const int32_t* src, const int32_t* dst, int32_t n, void* stream) {
@@ -462,7 +497,7 @@ xlpk_status xlpk_pages_copy(const xlpk_page_pool* p, const int32_t* src, const i
     l.n = std::min(kListPairs, n - i);
     std::copy_n(src + i, l.n, l.src);
     std::copy_n(dst + i, l.n, l.dst);
-    copy_kernel<<<sms * 4, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(*p, l);
+    copy_kernel<<<sms * kCopyCtas, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(*p, l);
   }
   XLPK_CUDA(cudaGetLastError());
   return XLPK_OK;
