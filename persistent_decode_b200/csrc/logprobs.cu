@@ -15,9 +15,10 @@ using namespace xlpk;
 namespace {
 
 constexpr int kMaxTop = 64;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kGroups = 128;       // groups of threads, each known by its largest logit
 constexpr int kPushed = 2048;     // candidates that fit while the row streams by
 constexpr int kRanked = 1024;     // candidates that fit at the end
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,7 +83,7 @@ __device__ inline Stat join(Stat a, Stat b) {
 template <class T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
-  static constexpr int U = sizeof(T) == 4 ? 8 : 4;   // vectors a thread has in flight: 32 logits
+  static constexpr int U = sizeof(T) == 4 ? 4 : 2;   // vectors of a round: 16 logits; the next round's are in flight meanwhile
   uint4 v;
   __device__ float operator[](int i) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -103,19 +104,25 @@ struct Shared {
   unsigned long long lists[kMaxCluster][kMaxTop];   // the leader's: every part's top tokens
   Stat stats[kMaxCluster];
   int befores[kMaxCluster];
-  uint32_t groups[2 * kMaxTop];                     // largest key of each group of threads
+  uint32_t groups[kGroups];                         // largest key of each group
+  uint32_t bar;                                     // key: at least top_k + 1 groups have a larger one or this
   Stat warp_stats[kWarps];
   int warp_befores[kWarps], warp_counts[kWarps];
   unsigned long long best[kWarps];
   int n_pushed, n_ranked;
 };
 
-// The least of the groups' largest keys.  Each group holds a logit at least that large, so with
-// more groups than alternatives nothing smaller can be one of them.
-__device__ inline uint32_t least_group(const Shared& sh, int groups) {
-  uint32_t k = 0xffffffffu;
-  for (int i = threadIdx.x & 31; i < groups; i += 32) k = min(k, *const_cast<const volatile uint32_t*>(&sh.groups[i]));
-  return __reduce_min_sync(~0u, k);
+// Raises the bar to the (top_k + 1)-th largest of the groups' keys.  Keys only rise while
+// this reads them, so whatever it finds is a bar that held at some time, and one that held
+// once holds for good: top_k logits are at least that large, and ties are looked after at
+// the end.  Threads 0 .. kGroups - 1 call it.
+__device__ inline void raise_bar(Shared& sh, int top_k) {
+  const volatile uint32_t* g = sh.groups;
+  const uint32_t mine = g[threadIdx.x];
+  int at_least = 0;
+#pragma unroll 8
+  for (int i = 0; i < kGroups; ++i) at_least += g[i] >= mine;
+  if (at_least > top_k && mine > sh.bar) atomicMax(&sh.bar, mine);
 }
 // What a logit must not be <= to be pushed (NaN: everything is).
 __device__ inline float bar_of(uint32_t key) { return key ? key_value(key) : __int_as_float(0x7fffffff); }
@@ -125,10 +132,10 @@ __device__ inline float bar_of(uint32_t key) { return key ? key_value(key) : __i
 template <class T, bool FULL>
 __device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int first, int there, int tok_vec, float bar_ge,
                                     float bar_gt) {
-  constexpr int N = Vec<T>::N, U = Vec<T>::U;
+  constexpr int N = Vec<T>::N;
   float mine = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < Vec<T>::U; ++u)
     if (FULL || u < there)
 #pragma unroll
       for (int i = 0; i < N; ++i) mine = fmaxf(mine, v[u][i]);
@@ -143,7 +150,7 @@ __device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int
     }
     // the maximum stands here: its ties are counted, not added
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < Vec<T>::U; ++u)
       if (FULL || u < there)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -159,7 +166,7 @@ __device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int
         }
   } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < Vec<T>::U; ++u)
       if (FULL || u < there)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -169,7 +176,7 @@ __device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int
         }
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int u = 0; u < Vec<T>::U; ++u)
     if (FULL || u < there) {
       const float bar = first + u * kThreads < tok_vec ? bar_ge : bar_gt;
 #pragma unroll
@@ -178,19 +185,34 @@ __device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int
   return mine;
 }
 
-// Pushes the round's logits that the bar lets through.
+// Pushes the round's logits that the bar lets through (all lanes of a warp call it).
 template <class T>
 __device__ inline void push(const Vec<T> (&v)[Vec<T>::U], int first, int there, int pre, float bar, Shared& sh) {
   constexpr int N = Vec<T>::N;
+  int n = 0;
 #pragma unroll
   for (int u = 0; u < Vec<T>::U; ++u)
-    if (u < there)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (!(v[u][i] <= bar)) {
-          const int at = atomicAdd(&sh.n_pushed, 1);
-          if (at < kPushed) sh.pushed[at] = place(v[u][i], pre + (first + u * kThreads) * N + i);
-        }
+    for (int i = 0; i < N; ++i) n += u < there && !(v[u][i] <= bar);
+  // one reservation for the warp
+  const int lane = threadIdx.x & 31;
+  int at = n;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, at, o);
+    if (lane >= o) at += y;
+  }
+  int base = 0;
+  if (lane == 31) base = atomicAdd(&sh.n_pushed, at);
+  at += __shfl_sync(~0u, base, 31) - n;
+  if (n == 0) return;
+#pragma unroll
+  for (int u = 0; u < Vec<T>::U; ++u)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (u < there && !(v[u][i] <= bar)) {
+        if (at < kPushed) sh.pushed[at] = place(v[u][i], pre + (first + u * kThreads) * N + i);
+        ++at;
+      }
 }
 
 // Ranks a list in shared memory: out[0 .. top_k) gets its largest, the rest of out is left.
@@ -198,20 +220,42 @@ __device__ inline void rank_list(const unsigned long long* list, int n, int top_
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const unsigned long long mine = list[i];
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) r += list[j] > mine;
     if (r < top_k) out[r] = mine;
   }
 }
 
+// The same for `parts` lists of top_k in descending order, by a search in each.
+__device__ inline void rank_sorted(const unsigned long long (&lists)[kMaxCluster][kMaxTop], int parts, int top_k,
+                                   unsigned long long* out) {
+  for (int i = threadIdx.x; i < parts * top_k; i += kThreads) {
+    const int p = i / top_k, k = i - p * top_k;
+    const unsigned long long mine = lists[p][k];
+    int r = k;
+    for (int q = 0; q < parts && r < top_k; ++q) {
+      if (q == p) continue;
+      int lo = 0, hi = top_k;   // the first that is not larger
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (lists[q][mid] > mine) lo = mid + 1;
+        else hi = mid;
+      }
+      r += lo;
+    }
+    if (r < top_k && mine) out[r] = mine;   // (place 0 fills up a part that is shorter than top_k)
+  }
+}
+
 // One cluster per row, its CTAs taking consecutive parts.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, int vocab, long long stride, const int* tokens,
-                                                               int top_k, int groups, int parts, float* logprob,
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, int vocab, long long stride, const int* tokens,
+                                                               int top_k, int parts, float* logprob,
                                                                float* entropy, int* rank, int* top_ids,
                                                                float* top_logprobs) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& sh = *reinterpret_cast<Shared*>(raw);
-  constexpr int N = Vec<T>::N, U = Vec<T>::U;
+  constexpr int N = Vec<T>::N;
   const long long r = blockIdx.x / parts;
   const int part = blockIdx.x - static_cast<int>(r) * parts;
   const T* x = logits + r * stride;
@@ -223,23 +267,25 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, 
             v1 = static_cast<int>(static_cast<long long>(vecs) * (part + 1) / parts);
   const uint4* body = reinterpret_cast<const uint4*>(x + pre);
 
-  Vec<T> v[U];
-  const auto load = [&](int first) {
+  Vec<T> v[Vec<T>::U], next[Vec<T>::U];
+  const auto load = [&](Vec<T>(&to)[Vec<T>::U], int from) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (first + u * kThreads < v1) {
+    for (int u = 0; u < Vec<T>::U; ++u)
+      if (from + u * kThreads < v1) {
         asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v[u].v.x), "=r"(v[u].v.y), "=r"(v[u].v.z), "=r"(v[u].v.w)
-                     : "l"(body + first + u * kThreads));
+                     : "=r"(to[u].v.x), "=r"(to[u].v.y), "=r"(to[u].v.z), "=r"(to[u].v.w)
+                     : "l"(body + from + u * kThreads));
       }
   };
+  constexpr int kStep = Vec<T>::U * kThreads;
   int first = v0 + threadIdx.x;
-  load(first);
+  load(v, first);
+  load(next, first + kStep);
   const int tok = tokens[r];
   const bool valid = tok >= 0 && tok < vocab;
   const float mine = valid ? static_cast<float>(x[tok]) : 0.f;
-  if (threadIdx.x < 2 * kMaxTop) sh.groups[threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.n_pushed = sh.n_ranked = 0;
+  if (threadIdx.x < kGroups) sh.groups[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.n_pushed = sh.n_ranked = 0, sh.bar = 0;
   __syncthreads();
 
   // A logit comes before the token's if it is not <= gt, or, to the left of the token, not <= ge: the
@@ -268,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, 
       }
       g.before = !(e <= (end_at < tok ? bar_ge : bar_gt));
       if (top_k > 0) {
-        atomicMax(&sh.groups[threadIdx.x % groups], order_key(e));
+        atomicMax(&sh.groups[threadIdx.x % kGroups], order_key(e));
         const int at = atomicAdd(&sh.n_pushed, 1);
         sh.pushed[at] = place(e, end_at);   // at most 14
       }
@@ -276,20 +322,37 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, 
   }
 
   // ---- the row streams by
-  for (int base = v0; base < v1 || base == v0; base += U * kThreads) {
-    const int there = min(U, max(0, (v1 - first + kThreads - 1) / kThreads));
-    const float top = __all_sync(~0u, there == U) ? round_stats<T, true>(g, v, first, there, tok_vec, bar_ge, bar_gt)
-                                                  : round_stats<T, false>(g, v, first, there, tok_vec, bar_ge, bar_gt);
+  int round = 0;
+  const auto take = [&](const Vec<T>(&now)[Vec<T>::U]) {
+    const int there = min(Vec<T>::U, max(0, (v1 - first + kThreads - 1) / kThreads));
+    const float top = __all_sync(~0u, there == Vec<T>::U) ? round_stats<T, true>(g, now, first, there, tok_vec, bar_ge, bar_gt)
+                                                        : round_stats<T, false>(g, now, first, there, tok_vec, bar_ge, bar_gt);
     if (top_k > 0) {
-      // the groups' maxima only rise: a thread below the bar raises none that matters
-      if (there > 0 && !(top <= bar_of(base == v0 ? 0 : least_group(sh, groups))))
-        atomicMax(&sh.groups[threadIdx.x % groups], order_key(top));
-      if (base == v0) __syncthreads();   // every group has its first logit
-      const float bar = bar_of(least_group(sh, groups));
-      if (!(top <= bar) || g.t != g.t) push(v, first, there, pre, bar, sh);   // (a NaN is pushed whatever the maximum)
+      // a thread below the bar has nothing that could raise it
+      if (there > 0 && !(top <= bar_of(*const_cast<volatile uint32_t*>(&sh.bar))))
+        atomicMax(&sh.groups[threadIdx.x % kGroups], order_key(top));
+      if (round == 0) __syncthreads();   // every group has its first logit
+      // (each time the row seen so far has doubled)
+      if ((round & (round + 1)) == 0 && threadIdx.x < kGroups) raise_bar(sh, top_k);
+      if (round == 0) __syncthreads();
+      const float bar = bar_of(*const_cast<volatile uint32_t*>(&sh.bar));
+      // a NaN is pushed whatever the maximum
+      if (__any_sync(~0u, !(top <= bar) || g.t != g.t)) push(now, first, there, pre, bar, sh);
     }
-    first += U * kThreads;
-    load(first);
+    ++round;
+    first += kStep;
+  };
+  for (int base = v0;;) {
+    take(v);
+    load(v, first + kStep);
+    if ((base += kStep) >= v1) break;
+    take(next);
+    load(next, first + kStep);
+    if ((base += kStep) >= v1) break;
+  }
+  if (top_k > 0) {
+    __syncthreads();
+    if (threadIdx.x < kGroups) raise_bar(sh, top_k);
   }
 
   // ---- this part's statistics
@@ -327,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, 
   const int want = min(top_k, hi - lo);
   unsigned long long* const out = sh.lists[0];
   if (top_k > 0) {
-    const uint32_t least = least_group(sh, groups);
+    const uint32_t least = sh.bar;
     const int n = sh.n_pushed;
     bool slow = n > kPushed;
     if (!slow) {
@@ -420,14 +483,10 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const T* logits, 
     }
   }
   if (top_k == 0) return;
-  // place 0 of a part that is shorter than top_k loses to every token
   if (parts > 1) {
-    for (int i = threadIdx.x; i < parts * top_k; i += kThreads) {
-      const int p = i / top_k, k = i - p * top_k;
-      sh.pushed[i] = p == 0 && k >= want ? 0 : sh.lists[p][k];
-    }
+    if (static_cast<int>(threadIdx.x) >= want && static_cast<int>(threadIdx.x) < top_k) out[threadIdx.x] = 0;
     __syncthreads();
-    rank_list(sh.pushed, parts * top_k, top_k, sh.ranked);
+    rank_sorted(sh.lists, parts, top_k, sh.ranked);
   }
   __syncthreads();
   const unsigned long long* const list = parts > 1 ? sh.ranked : out;
@@ -443,7 +502,7 @@ template <class T>
 xlpk_status launch(const T* logits, long long rows, int vocab, long long stride, const int* tokens, int top_k, float* logprob,
                    float* entropy, int* rank, int* top_ids, float* top_logprobs, int sms, cudaStream_t st) {
   int parts = 1;
-  while (parts < kMaxCluster && rows * parts * 2 <= 2 * sms && vocab / (parts * 2) >= kThreads * Vec<T>::N) parts *= 2;
+  while (parts < kMaxCluster && rows * parts * 2 <= 4 * sms && vocab / (parts * 2) >= kThreads * Vec<T>::N) parts *= 2;
   static std::atomic<unsigned long long> ready;   // devices whose kernel has its attributes
   int dev = 0;
   XLPK_CUDA(cudaGetDevice(&dev));
@@ -463,8 +522,7 @@ xlpk_status launch(const T* logits, long long rows, int vocab, long long stride,
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   c.attrs = &cluster;
   c.numAttrs = 1;
-  const int groups = (top_k + 16) / 16 * 16;   // more than top_k
-  XLPK_CUDA(cudaLaunchKernelEx(&c, logprobs_kernel<T>, logits, vocab, stride, tokens, top_k, groups, parts, logprob, entropy,
+  XLPK_CUDA(cudaLaunchKernelEx(&c, logprobs_kernel<T>, logits, vocab, stride, tokens, top_k, parts, logprob, entropy,
                                rank, top_ids, top_logprobs));
   return XLPK_OK;
 }
