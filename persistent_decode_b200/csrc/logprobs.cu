@@ -18,10 +18,14 @@ constexpr int kMaxTop = 64;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kGroups = 128;       // groups of threads, each known by its largest logit
-constexpr int kPushed = 2048;     // candidates that fit while the row streams by
-constexpr int kRanked = 1024;     // candidates that fit at the end
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kGroups = 128;       // most groups of threads, each known by its largest logit
+constexpr int kMarks = 64;         // stretches of rounds that a warp knows the largest logit of
+constexpr int kUnroll = 4;         // 16-byte vectors a thread takes in a round
+constexpr int kStages = 3;         // rounds on their way
+constexpr int kStep = kUnroll * kThreads;
+constexpr int kPushed = 512;       // candidates that are ranked at most
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFar = 1e38f;      // a maximum this far out has no neighbour within 2^100: all others weigh 0
 
 // A logit's place in descending order: larger keys come first, NaN before +inf,
 // -0 equals +0; ties go to the lower index.  No value has key 0.
@@ -31,6 +35,8 @@ __device__ inline uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ inline float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+// The key below k (no value has the key of -0).
+__device__ inline uint32_t key_below(uint32_t k) { return k - (k == 0x80000000u ? 2 : 1); }
 __device__ inline unsigned long long place(float x, int i) {
   return static_cast<unsigned long long>(order_key(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
 }
@@ -48,9 +54,9 @@ __device__ inline float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ inline float warp_max(float x) {
+__device__ inline float warp_max_nan(float x) {
   float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ inline float warp_sum(float x) {
@@ -60,7 +66,8 @@ __device__ inline float warp_sum(float x) {
 
 // Softmax statistics of a set of logits: the maximum m, and of all others (the
 // maximum itself counts 1 and 0, exactly) s = sum e^(x-m), t = sum e^(x-m) (x-m).
-// The others are kept apart so that log(1 + s) keeps a small s.
+// The others are kept apart so that log(1 + s) keeps a small s.  NaN in t: the
+// set holds NaN or +inf.
 struct Stat {
   float m, s, t;
 };
@@ -83,136 +90,154 @@ __device__ inline Stat join(Stat a, Stat b) {
 template <class T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
-  static constexpr int U = sizeof(T) == 4 ? 4 : 2;   // vectors of a round: 16 logits; the next round's are in flight meanwhile
+  static constexpr uint32_t NONE = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;   // -inf
   uint4 v;
   __device__ float operator[](int i) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if (sizeof(T) == 4) return __uint_as_float(w[i]);
     return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+  // NaN if there is one
+  __device__ float largest() const {
+    if (sizeof(T) == 4) return max_nan(max_nan((*this)[0], (*this)[1]), max_nan((*this)[2], (*this)[3]));
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+    return max_nan(__low2float(m), __high2float(m));
+  }
 };
 
-// What one thread gathers of its part of a row.
+// What one thread gathers of its part of a row.  Terms are kept as powers of 2: with
+// y = x log2(e) - base, rounded once, s = sum 2^y and t = sum 2^y y over the logits below
+// the warp's maximum m; base is m log2(e) rounded, and what that leaves, y of m itself, is
+// put right at the end.  Against x - m, a product and an exponential this saves an instruction
+// for each logit.
 struct Gather {
-  float m = -INFINITY, s = 0.f, t = 0.f;   // m is the warp's; s and t of logits below it
-  int ties = 0;                            // logits equal to m
-  int before = 0;                          // logits that come before the token's
+  float m = -INFINITY, base = 0.f, s = 0.f, t = 0.f;
+  int ties = 0;            // logits equal to m
+  int before = 0;          // logits that come before the token's
+  bool careful = false;    // logits of -inf have been met: 2^y y is 0 times infinity
+
+  __device__ float own() const { return fmaf(m, kLog2e, -base); }
+  // A logit that may be the maximum; NaN, and +inf, leave NaN in t.
+  __device__ void any(float x) {
+    if (x < m) {
+      const float y = fmaxf(fmaf(x, kLog2e, -base), -1000.f), e = ex2(y);
+      s += e;
+      t += e * y;
+    } else {
+      ++ties;
+      t += x - m;
+    }
+  }
+  __device__ void rise(float top) {
+    const float up = fminf(fmaxf(top * kLog2e, -3e38f), 3e38f);
+    if (fabsf(m) < kFar) {
+      const float y = own(), e = ties * ex2(y), d = base - up, w = ex2(d);
+      t += e * y;
+      s += e;
+      t = w > 0.f ? w * (t + d * s) : w * t;
+      s *= w;
+    } else {
+      s = 0.f;
+      t = t != t ? t : 0.f;
+    }
+    ties = 0;
+    m = top;
+    base = up;
+  }
 };
 
-struct Shared {
-  unsigned long long pushed[kPushed], ranked[kRanked];
+constexpr int kQueueBytes = kStages * kStep * 16;
+
+struct alignas(16) Shared {
+  unsigned long long pushed[kMaxCluster * kMaxTop];
   unsigned long long lists[kMaxCluster][kMaxTop];   // the leader's: every part's top tokens
+  float marks[kWarps][kMarks];
+  uint32_t groups[kGroups];                         // largest key of each group
   Stat stats[kMaxCluster];
   int befores[kMaxCluster];
-  uint32_t groups[kGroups];                         // largest key of each group
   uint32_t bar;                                     // key: at least top_k + 1 groups have a larger one or this
   Stat warp_stats[kWarps];
   int warp_befores[kWarps], warp_counts[kWarps];
   unsigned long long best[kWarps];
-  int n_pushed, n_ranked;
+  int n_pushed;
 };
+static_assert(kPushed <= kMaxCluster * kMaxTop, "candidates");
 
-// Raises the bar to the (top_k + 1)-th largest of the groups' keys.  Keys only rise while
-// this reads them, so whatever it finds is a bar that held at some time, and one that held
-// once holds for good: top_k logits are at least that large, and ties are looked after at
-// the end.  Threads 0 .. kGroups - 1 call it.
-__device__ inline void raise_bar(Shared& sh, int top_k) {
-  const volatile uint32_t* g = sh.groups;
-  const uint32_t mine = g[threadIdx.x];
+// Statistics and rank of one round: the thread's vectors, those past the part's end all -inf,
+// which adds nothing to either (`left`: the vectors wholly to the left of the token that the part
+// has); `top` the warp's largest logit, or NaN.
+template <class T>
+__device__ inline void round_stats(Gather& g, const Vec<T> (&v)[kUnroll], float top, int first, int left, float bar_ge,
+                                   float bar_gt) {
+  constexpr int N = Vec<T>::N;
+  if (top >= g.m) {
+    // the maximum stands here: its ties are counted, not added
+    if (top > g.m) g.rise(top);
+    if (top > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) g.any(v[u][i]);
+    }
+  } else {
+    float s = 0.f, t = 0.f;
+    if (!g.careful) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float y = fmaf(v[u][i], kLog2e, -g.base), e = ex2(y);
+          s += e;
+          t = fmaf(e, y, t);
+        }
+      g.careful = t != t;
+    }
+    if (g.careful) {
+      s = t = 0.f;
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float y = max_nan(fmaf(v[u][i], kLog2e, -g.base), -1000.f), e = ex2(y);
+          s += e;
+          t = fmaf(e, y, t);
+        }
+    }
+    g.s += s;
+    g.t += t;
+  }
+  if (!(top < bar_gt)) {   // (bar_gt is the token's logit: few rounds have larger ones if it is a likely token)
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const float bar = first + u * kThreads < left ? bar_ge : bar_gt;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t larger;
+        asm("set.gtu.u32.f32 %0, %1, %2;" : "=r"(larger) : "f"(v[u][i]), "f"(bar));
+        g.before -= static_cast<int>(larger);
+      }
+    }
+  }
+}
+
+// Raises the bar to the (top_k + 1)-th largest of the groups' keys: at least so many logits
+// are that large, so no smaller one is an alternative.  Threads 0 .. groups - 1 call it.
+__device__ inline void raise_bar(Shared& sh, int groups, int top_k) {
+  const uint4* keys = reinterpret_cast<const uint4*>(sh.groups);
+  const uint32_t mine = sh.groups[threadIdx.x];
   int at_least = 0;
 #pragma unroll 8
-  for (int i = 0; i < kGroups; ++i) at_least += g[i] >= mine;
-  if (at_least > top_k && mine > sh.bar) atomicMax(&sh.bar, mine);
-}
-// What a logit must not be <= to be pushed (NaN: everything is).
-__device__ inline float bar_of(uint32_t key) { return key ? key_value(key) : __int_as_float(0x7fffffff); }
-
-// Statistics and rank of one round: U vectors of each thread (FULL: all of them are there).
-// Returns the thread's largest logit.
-template <class T, bool FULL>
-__device__ inline float round_stats(Gather& g, const Vec<T> (&v)[Vec<T>::U], int first, int there, int tok_vec, float bar_ge,
-                                    float bar_gt) {
-  constexpr int N = Vec<T>::N;
-  float mine = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < Vec<T>::U; ++u)
-    if (FULL || u < there)
-#pragma unroll
-      for (int i = 0; i < N; ++i) mine = fmaxf(mine, v[u][i]);
-  const float top = warp_max(mine);
-  if (top >= g.m) {
-    if (top > g.m) {
-      const float d = g.m - top, w = ex2(d * kLog2e), all = g.s + g.ties;
-      g.t = w > 0.f ? w * (g.t + d * all) : w * g.t;   // (d may be -inf)
-      g.s = w * all;
-      g.ties = 0;
-      g.m = top;
-    }
-    // the maximum stands here: its ties are counted, not added
-#pragma unroll
-    for (int u = 0; u < Vec<T>::U; ++u)
-      if (FULL || u < there)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float x = v[u][i];
-          if (top == -INFINITY) {
-            if (x != x) g.t = x;
-          } else {
-            const float d = max_nan(x - top, -1000.f), e = ex2(d * kLog2e);
-            if (x < top) g.s += e;
-            else ++g.ties;
-            g.t += e * d;
-          }
-        }
-  } else {
-#pragma unroll
-    for (int u = 0; u < Vec<T>::U; ++u)
-      if (FULL || u < there)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float d = max_nan(v[u][i] - g.m, -1000.f), e = ex2(d * kLog2e);   // (e * d is 0 for -inf too)
-          g.s += e;
-          g.t += e * d;
-        }
+  for (int i = 0; i < groups / 4; ++i) {
+    const uint4 k = keys[i];
+    at_least += (k.x >= mine) + (k.y >= mine) + (k.z >= mine) + (k.w >= mine);
   }
-#pragma unroll
-  for (int u = 0; u < Vec<T>::U; ++u)
-    if (FULL || u < there) {
-      const float bar = first + u * kThreads < tok_vec ? bar_ge : bar_gt;
-#pragma unroll
-      for (int i = 0; i < N; ++i) g.before += !(v[u][i] <= bar);
-    }
-  return mine;
+  if (at_least > top_k) atomicMax(&sh.bar, mine);
 }
 
-// Pushes the round's logits that the bar lets through (all lanes of a warp call it).
-template <class T>
-__device__ inline void push(const Vec<T> (&v)[Vec<T>::U], int first, int there, int pre, float bar, Shared& sh) {
-  constexpr int N = Vec<T>::N;
-  int n = 0;
-#pragma unroll
-  for (int u = 0; u < Vec<T>::U; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i) n += u < there && !(v[u][i] <= bar);
-  // one reservation for the warp
-  const int lane = threadIdx.x & 31;
-  int at = n;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, at, o);
-    if (lane >= o) at += y;
-  }
-  int base = 0;
-  if (lane == 31) base = atomicAdd(&sh.n_pushed, at);
-  at += __shfl_sync(~0u, base, 31) - n;
-  if (n == 0) return;
-#pragma unroll
-  for (int u = 0; u < Vec<T>::U; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (u < there && !(v[u][i] <= bar)) {
-        if (at < kPushed) sh.pushed[at] = place(v[u][i], pre + (first + u * kThreads) * N + i);
-        ++at;
-      }
+__device__ inline void push(Shared& sh, float x, int index) {
+  const int at = atomicAdd(&sh.n_pushed, 1);
+  if (at < kPushed) sh.pushed[at] = place(x, index);
 }
 
 // Ranks a list in shared memory: out[0 .. top_k) gets its largest, the rest of out is left.
@@ -226,33 +251,11 @@ __device__ inline void rank_list(const unsigned long long* list, int n, int top_
   }
 }
 
-// The same for `parts` lists of top_k in descending order, by a search in each.
-__device__ inline void rank_sorted(const unsigned long long (&lists)[kMaxCluster][kMaxTop], int parts, int top_k,
-                                   unsigned long long* out) {
-  for (int i = threadIdx.x; i < parts * top_k; i += kThreads) {
-    const int p = i / top_k, k = i - p * top_k;
-    const unsigned long long mine = lists[p][k];
-    int r = k;
-    for (int q = 0; q < parts && r < top_k; ++q) {
-      if (q == p) continue;
-      int lo = 0, hi = top_k;   // the first that is not larger
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (lists[q][mid] > mine) lo = mid + 1;
-        else hi = mid;
-      }
-      r += lo;
-    }
-    if (r < top_k && mine) out[r] = mine;   // (place 0 fills up a part that is shorter than top_k)
-  }
-}
-
 // One cluster per row, its CTAs taking consecutive parts.
 template <class T>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, int vocab, long long stride, const int* tokens,
-                                                               int top_k, int parts, float* logprob,
-                                                               float* entropy, int* rank, int* top_ids,
-                                                               float* top_logprobs) {
+__global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, int vocab, long long stride, const int* tokens,
+                                                               int top_k, int parts, float* logprob, float* entropy, int* rank,
+                                                               int* top_ids, float* top_logprobs) {
   extern __shared__ __align__(16) uint8_t raw[];
   Shared& sh = *reinterpret_cast<Shared*>(raw);
   constexpr int N = Vec<T>::N;
@@ -265,117 +268,116 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
   const int pre = min(vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
   const int vecs = (vocab - pre) / N, v0 = static_cast<int>(static_cast<long long>(vecs) * part / parts),
             v1 = static_cast<int>(static_cast<long long>(vecs) * (part + 1) / parts);
-  const uint4* body = reinterpret_cast<const uint4*>(x + pre);
+  const int lo = part == 0 ? 0 : pre + v0 * N, hi = part == parts - 1 ? vocab : pre + v1 * N;
+  const uint4* const body = reinterpret_cast<const uint4*>(x + pre);
 
-  Vec<T> v[Vec<T>::U], next[Vec<T>::U];
-  const auto load = [&](Vec<T>(&to)[Vec<T>::U], int from) {
+  // Every thread copies the bytes that it reads itself, so its own wait is the only one.
+  Vec<T>* const queue = reinterpret_cast<Vec<T>*>(raw + sizeof(Shared)) + threadIdx.x;
+  const uint32_t queue_at = static_cast<uint32_t>(__cvta_generic_to_shared(queue));
+  const auto fetch = [&](int from, int stage) {
 #pragma unroll
-    for (int u = 0; u < Vec<T>::U; ++u)
-      if (from + u * kThreads < v1) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(to[u].v.x), "=r"(to[u].v.y), "=r"(to[u].v.z), "=r"(to[u].v.w)
-                     : "l"(body + from + u * kThreads));
-      }
+    for (int u = 0; u < kUnroll; ++u)
+      if (from + u * kThreads < v1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(queue_at + (stage * kStep + u * kThreads) * 16),
+                     "l"(body + from + u * kThreads)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  constexpr int kStep = Vec<T>::U * kThreads;
-  int first = v0 + threadIdx.x;
-  load(v, first);
-  load(next, first + kStep);
+  const int mine0 = v0 + threadIdx.x;   // the thread's first vector
+  for (int i = 0; i < kStages; ++i) fetch(mine0 + i * kStep, i);
   const int tok = tokens[r];
   const bool valid = tok >= 0 && tok < vocab;
   const float mine = valid ? static_cast<float>(x[tok]) : 0.f;
   if (threadIdx.x < kGroups) sh.groups[threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.n_pushed = sh.n_ranked = 0, sh.bar = 0;
+  if (threadIdx.x == 0) sh.n_pushed = 0, sh.bar = 0;
   __syncthreads();
 
   // A logit comes before the token's if it is not <= gt, or, to the left of the token, not <= ge: the
   // float below the token's (NaN, and so everything, if there is none).  tok_vec: the vectors wholly to the left.
-  const int tok_vec = tok < pre ? 0 : (tok - pre) / N;
+  const int tok_vec = tok < pre ? 0 : (tok - pre) / N, left = min(tok_vec, v1);
   const uint32_t my_key = order_key(mine);
-  const float bar_gt = mine, bar_ge = mine == -INFINITY ? __int_as_float(0x7fffffff)
-                                                        : key_value(my_key - (my_key == 0x80000000u ? 2 : 1));   // (no -0)
+  const float bar_gt = mine, bar_ge = mine == -INFINITY ? __int_as_float(0x7fffffff) : key_value(key_below(my_key));
 
   // the ends, one logit of a thread at most
   Gather g;
+  float best = -INFINITY;   // the thread's largest logit, or NaN
   int end_at = -1;
   if (part == 0 && static_cast<int>(threadIdx.x) < pre) end_at = threadIdx.x;
   if (part == parts - 1 && static_cast<int>(threadIdx.x) >= 32 && pre + vecs * N + static_cast<int>(threadIdx.x) - 32 < vocab)
     end_at = pre + vecs * N + threadIdx.x - 32;
+  const float end = end_at >= 0 ? static_cast<float>(x[end_at]) : -INFINITY;
   if (warp < 2) {
-    const float e = end_at >= 0 ? static_cast<float>(x[end_at]) : -INFINITY;
-    g.m = warp_max(e);
+    const float top = warp_max_nan(end);
+    if (top > -INFINITY) g.rise(top);
     if (end_at >= 0) {
-      if (e != e) g.t = e;
-      else if (g.m > -INFINITY) {
-        const float d = fmaxf(e - g.m, -1000.f), w = ex2(d * kLog2e);
-        if (e < g.m) g.s = w;
-        else g.ties = 1;
-        g.t = e == g.m ? e - e : w * d;   // (+inf: NaN)
-      }
-      g.before = !(e <= (end_at < tok ? bar_ge : bar_gt));
-      if (top_k > 0) {
-        atomicMax(&sh.groups[threadIdx.x % kGroups], order_key(e));
-        const int at = atomicAdd(&sh.n_pushed, 1);
-        sh.pushed[at] = place(e, end_at);   // at most 14
-      }
+      if (top > -INFINITY) g.any(end);
+      g.before = !(end <= (end_at < tok ? bar_ge : bar_gt));
+      best = end;
     }
+    if (top != top) g.t = top;
   }
 
   // ---- the row streams by
-  int round = 0;
-  const auto take = [&](const Vec<T>(&now)[Vec<T>::U]) {
-    const int there = min(Vec<T>::U, max(0, (v1 - first + kThreads - 1) / kThreads));
-    const float top = __all_sync(~0u, there == Vec<T>::U) ? round_stats<T, true>(g, now, first, there, tok_vec, bar_ge, bar_gt)
-                                                        : round_stats<T, false>(g, now, first, there, tok_vec, bar_ge, bar_gt);
-    if (top_k > 0) {
-      // a thread below the bar has nothing that could raise it
-      if (there > 0 && !(top <= bar_of(*const_cast<volatile uint32_t*>(&sh.bar))))
-        atomicMax(&sh.groups[threadIdx.x % kGroups], order_key(top));
-      if (round == 0) __syncthreads();   // every group has its first logit
-      // (each time the row seen so far has doubled)
-      if ((round & (round + 1)) == 0 && threadIdx.x < kGroups) raise_bar(sh, top_k);
-      if (round == 0) __syncthreads();
-      const float bar = bar_of(*const_cast<volatile uint32_t*>(&sh.bar));
-      // a NaN is pushed whatever the maximum
-      if (__any_sync(~0u, !(top <= bar) || g.t != g.t)) push(now, first, there, pre, bar, sh);
+  const int rounds = (v1 - v0 + kStep - 1) / kStep;
+  int shift = 0;
+  while (rounds >> shift >= kMarks) ++shift;   // rounds to a mark: 2^shift
+  int stage = 0, first = mine0;
+#pragma unroll 1
+  for (int round = 0; round < rounds; ++round, first += kStep) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    Vec<T> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = queue[stage * kStep + u * kThreads];
+    if (round == rounds - 1) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (first + u * kThreads >= v1) v[u].v = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
     }
-    ++round;
-    first += kStep;
-  };
-  for (int base = v0;;) {
-    take(v);
-    load(v, first + kStep);
-    if ((base += kStep) >= v1) break;
-    take(next);
-    load(next, first + kStep);
-    if ((base += kStep) >= v1) break;
-  }
-  if (top_k > 0) {
-    __syncthreads();
-    if (threadIdx.x < kGroups) raise_bar(sh, top_k);
+    float top = v[0].largest();
+#pragma unroll
+    for (int u = 1; u < kUnroll; ++u) top = max_nan(top, v[u].largest());
+    best = max_nan(best, top);
+    top = warp_max_nan(top);
+    if (lane == 0) {
+      float* mark = &sh.marks[warp][round >> shift];
+      *mark = round & ((1 << shift) - 1) ? max_nan(*mark, top) : top;
+    }
+    round_stats<T>(g, v, top, first, left, bar_ge, bar_gt);
+    // (a part that fits in the queue stays there)
+    if (round + kStages < rounds) fetch(first + kStages * kStep, stage);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 
   // ---- this part's statistics
   {
-    const float s = warp_sum(g.s), t = warp_sum(g.t);
+    float s = warp_sum(g.s), t = warp_sum(g.t);
     const int ties = __reduce_add_sync(~0u, g.ties), before = __reduce_add_sync(~0u, g.before);
+    if (fabsf(g.m) < kFar) {
+      const float y = g.own(), f = ex2(-y);
+      t = (t - y * s) * f * kLn2;
+      s = s * f + (ties - 1);
+    } else {
+      s = g.m == -INFINITY ? 0.f : static_cast<float>(ties - 1);
+      t = t != t ? t : 0.f;
+    }
     if (lane == 0) {
-      sh.warp_stats[warp] = {g.m, s + (ties - 1), t};
-      if (g.m == -INFINITY) sh.warp_stats[warp].s = 0.f;
+      sh.warp_stats[warp] = {g.m, s, t};
       sh.warp_befores[warp] = before;
     }
   }
+  const int groups = top_k < kGroups / 4 ? kGroups / 2 : kGroups;   // about twice top_k or more
+  if (top_k > 0 && (mine0 < v1 || end_at >= 0)) atomicMax(&sh.groups[threadIdx.x & (groups - 1)], order_key(best));
   __syncthreads();
   Stat all = sh.warp_stats[0];
   int before = 0;
-  if (warp == 0) {
+  if (warp == kWarps - 1) {
     // joined in the order of the warps
     for (int w = 1; w < kWarps; ++w) all = join(all, sh.warp_stats[w]);
     before = __reduce_add_sync(~0u, lane < kWarps ? sh.warp_befores[lane] : 0);
     if (valid && mine != mine) {
       // a NaN's rank: the NaN to its left
       before = 0;
-      const int lo = part == 0 ? 0 : pre + v0 * N, hi = part == parts - 1 ? vocab : pre + v1 * N;
       for (int i = lo + lane; i < min(hi, tok); i += 32) before += order_key(static_cast<float>(x[i])) == my_key;
       before = __reduce_add_sync(~0u, before);
     } else if (valid && tok >= pre && tok_vec >= v0 && tok_vec < v1) {
@@ -386,29 +388,55 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
   }
 
   // ---- this part's top tokens, in order
-  const int lo = part == 0 ? 0 : pre + v0 * N, hi = part == parts - 1 ? vocab : pre + v1 * N;
   const int want = min(top_k, hi - lo);
   unsigned long long* const out = sh.lists[0];
   if (top_k > 0) {
-    const uint32_t least = sh.bar;
-    const int n = sh.n_pushed;
-    bool slow = n > kPushed;
-    if (!slow) {
-      for (int i = threadIdx.x; i < n; i += kThreads)
-        if (static_cast<uint32_t>(sh.pushed[i] >> 32) > least) {
-          const int at = atomicAdd(&sh.n_ranked, 1);
-          if (at < kRanked) sh.ranked[at] = sh.pushed[i];
+    if (static_cast<int>(threadIdx.x) < groups) raise_bar(sh, groups, top_k);
+    __syncthreads();
+    // The candidates are the logits that the bar lets through, found again where a warp's mark says
+    // that there are some: of 250 stretches about as many as there are alternatives.  (Listing them
+    // while the row streams by, under a bar that rises, took more instructions than the statistics:
+    // 1024 rows of 128256 with 20 alternatives 139 us.)  Logits equal to the bar are let through
+    // unless it is a mask's value (-inf or a type's lowest), of which there are too many.
+    const uint32_t bar_key = sh.bar;
+    bool strict = !(key_value(bar_key) > -3e38f), slow = false;   // (an empty bar, 0, lets everything through)
+    for (;;) {
+      const float bar = bar_key == 0 ? __int_as_float(0x7fffffff) : key_value(strict ? bar_key : key_below(bar_key));
+      if (end_at >= 0 && !(end <= bar)) push(sh, end, end_at);
+      for (int mark = 0; mark << shift < rounds; ++mark) {
+        if (sh.marks[warp][mark] <= bar) continue;
+        for (int round = mark << shift; round < min(rounds, (mark + 1) << shift); ++round) {
+#pragma unroll 1
+          for (int u = 0; u < kUnroll; ++u) {
+            const int at = mine0 + round * kStep + u * kThreads;
+            if (at >= v1) break;
+            Vec<T> v;
+            if (rounds <= kStages) v = queue[round * kStep + u * kThreads];
+            else v.v = body[at];
+            if (v.largest() <= bar) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (!(v[i] <= bar)) push(sh, v[i], pre + at * N + i);
+          }
+          if (*const_cast<volatile int*>(&sh.n_pushed) > kPushed) break;
         }
+      }
       __syncthreads();
-      slow = sh.n_ranked > kRanked;
+      slow = sh.n_pushed > kPushed;
+      if (!slow || strict) break;
+      // long ties: without them
+      strict = true;
+      __syncthreads();
+      if (threadIdx.x == 0) sh.n_pushed = 0;
+      __syncthreads();
     }
     if (!slow) {
-      const int above = sh.n_ranked;
-      rank_list(sh.ranked, above, want, out);
-      // logits equal to the bar (masked rows, long ties) are not pushed: the first of them fill what is missing
+      const int above = sh.n_pushed;
+      rank_list(sh.pushed, above, want, out);
+      // those equal to a strict bar are not listed: the first of them fill what is missing
       for (int base = lo, have = above; have < want && base < hi; base += kThreads) {
         const int i = base + threadIdx.x;
-        const bool same = i < hi && order_key(static_cast<float>(x[i])) == least;
+        const bool same = i < hi && order_key(static_cast<float>(x[i])) == bar_key;
         const uint32_t votes = __ballot_sync(~0u, same);
         if (lane == 0) sh.warp_counts[warp] = __popc(votes);
         __syncthreads();
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
         __syncthreads();
       }
     } else {
-      // more candidates than fit (rows in rising order, or of NaN): one search of the part for each
+      // more than are ranked even so (NaN, or large logits that all fall to few groups): one search of the part for each
       unsigned long long last = ~0ull;
       for (int k = 0; k < want; ++k) {
         unsigned long long b = 0;
@@ -457,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
         const unsigned long long p = static_cast<int>(threadIdx.x) < want ? out[threadIdx.x] : 0;
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at(&sh.lists[part][threadIdx.x])), "l"(p) : "memory");
       }
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == kThreads - 1) {
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at(&sh.stats[part].m)), "f"(all.m) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at(&sh.stats[part].s)), "f"(all.s) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at(&sh.stats[part].t)), "f"(all.t) : "memory");
@@ -468,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (part != 0) return;
   }
-  if (warp == 0) {
+  if (warp == kWarps - 1) {
     for (int p = 1; p < parts; ++p) {
       all = join(all, sh.stats[p]);
       before += sh.befores[p];
@@ -483,13 +511,27 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const T* logits, 
     }
   }
   if (top_k == 0) return;
+  const unsigned long long* list = out;
   if (parts > 1) {
-    if (static_cast<int>(threadIdx.x) >= want && static_cast<int>(threadIdx.x) < top_k) out[threadIdx.x] = 0;
+    // each part's list is in order: with its first `deep` entries no smaller than the least of
+    // their last, top_k entries are, and whatever is smaller than that is out
+    if (static_cast<int>(threadIdx.x) >= want && static_cast<int>(threadIdx.x) < top_k) out[threadIdx.x] = 0;   // (a short part)
+    if (threadIdx.x == 0) sh.n_pushed = 0;
     __syncthreads();
-    rank_sorted(sh.lists, parts, top_k, sh.ranked);
+    const int deep = (top_k + parts - 1) / parts;
+    unsigned long long least = ~0ull;
+    for (int p = 0; p < parts; ++p) least = min(least, sh.lists[p][deep - 1]);
+    for (int i = threadIdx.x; i < parts * top_k; i += kThreads) {
+      const unsigned long long c = sh.lists[i / top_k][i % top_k];
+      if (c && c >= least) sh.pushed[atomicAdd(&sh.n_pushed, 1)] = c;
+    }
+    __syncthreads();
+    const int n = sh.n_pushed;
+    __syncthreads();
+    rank_list(sh.pushed, n, top_k, sh.lists[1]);   // (all lists have been read)
+    list = sh.lists[1];
   }
   __syncthreads();
-  const unsigned long long* const list = parts > 1 ? sh.ranked : out;
   const float m = sh.stats[0].m, log_s = sh.stats[0].s;
   for (int k = threadIdx.x; k < top_k; k += kThreads) {
     const float v = key_value(static_cast<uint32_t>(list[k] >> 32));
@@ -502,19 +544,19 @@ template <class T>
 xlpk_status launch(const T* logits, long long rows, int vocab, long long stride, const int* tokens, int top_k, float* logprob,
                    float* entropy, int* rank, int* top_ids, float* top_logprobs, int sms, cudaStream_t st) {
   int parts = 1;
-  while (parts < kMaxCluster && rows * parts * 2 <= 4 * sms && vocab / (parts * 2) >= kThreads * Vec<T>::N) parts *= 2;
+  while (parts < kMaxCluster && rows * parts * 2 <= 3 * sms && vocab / (parts * 2) >= kThreads * Vec<T>::N) parts *= 2;
   static std::atomic<unsigned long long> ready;   // devices whose kernel has its attributes
   int dev = 0;
   XLPK_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
     XLPK_CUDA(cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-    XLPK_CUDA(cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared)));
+    XLPK_CUDA(cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared) + kQueueBytes));
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(static_cast<unsigned>(rows * parts));
   c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = sizeof(Shared);
+  c.dynamicSmemBytes = sizeof(Shared) + kQueueBytes;
   c.stream = st;
   cudaLaunchAttribute cluster{};
   cluster.id = cudaLaunchAttributeClusterDimension;
