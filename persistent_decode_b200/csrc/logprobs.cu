@@ -544,7 +544,7 @@ template <class T>
 xlpk_status launch(const T* logits, long long rows, int vocab, long long stride, const int* tokens, int top_k, float* logprob,
                    float* entropy, int* rank, int* top_ids, float* top_logprobs, int sms, cudaStream_t st) {
   int parts = 1;
-  while (parts < kMaxCluster && rows * parts * 2 <= 3 * sms && vocab / (parts * 2) >= kThreads * Vec<T>::N) parts *= 2;
+  while (parts < kMaxCluster && rows * parts * 2 <= 3 * sms && vocab / (parts * 2) >= 2 * kThreads * Vec<T>::N) parts *= 2;
   static std::atomic<unsigned long long> ready;   // devices whose kernel has its attributes
   int dev = 0;
   XLPK_CUDA(cudaGetDevice(&dev));
