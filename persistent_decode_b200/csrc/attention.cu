@@ -22,11 +22,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 256;
-constexpr int kTile = 16;   // positions a warp takes at a time
+constexpr int kTile = 16;   // positions of a tile; a warp takes two of its tiles at a time
 
 struct Args {
   xlpk_attention_args a;
   float* parts;     // [CTAs][2] slots of partial results
+  int page_shift;   // log2 of page_size, or -1
+  bool flat;        // a tile never crosses a page
   int4* joins;      // [CTAs] (sequence, kv head, last CTA, -) of the segment that CTA begins and another ends; .x < 0: none
 };
 
@@ -136,6 +138,12 @@ __device__ inline uint32_t widen(uint32_t codes) {
   return r;
 }
 
+__device__ inline uint32_t widen_high(uint32_t codes) {
+  uint32_t r;
+  asm("{ .reg .b16 h; mov.b32 {_, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(codes));
+  return r;
+}
+
 template <bool IO32, int N>
 __device__ inline void load_row(const void* base, long long at, float (&x)[N]) {
   if (IO32) {
@@ -190,6 +198,14 @@ __device__ inline void round_row(const float (&x)[N], float inv_scale, uint32_t*
   }
 }
 
+template <int BYTES>
+__device__ inline void copy_async(uint32_t dst, const void* src) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// Zeros unless `real`; then nothing is read.
 template <int BYTES>
 __device__ inline void copy_async(uint32_t dst, const void* src, bool real) {
   if (BYTES == 16)
@@ -284,15 +300,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   }
   if (count == 0) return;
 
-  // ---- the warp's queue of tiles in shared memory.  Every lane copies exactly the bytes that
-  // it multiplies, so a lane's own wait is the only one: no barrier, no shared index.
+  // ---- the warp's queue of tiles in shared memory.  K, and e4m3 V, are read by the lane that
+  // copied them; bf16 V is laid out in rows for ldmatrix, its 16-byte chunks swizzled.
   const uint32_t queue = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * S::STAGES * S::STAGE;
   const uint8_t* queue_at = smem + warp * S::STAGES * S::STAGE;
+  // where this lane puts chunk c of V row 2t + (r & 1) + 8 (r >> 1)
+  const auto v_slot = [&](int r, int c) {
+    if (S::KV8) return S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB;
+    const int row = 2 * t + (r & 1) + (r >> 1) * 8;
+    return S::KBYTES + row * D * 2 + (((c * 8 + g) ^ (row & 7)) & (D / 8 - 1)) * 16;
+  };
   Walk f = w;            // the tile that is fetched next
   f.i += warp;
   int page_f = -1, in_f = 0, bad_stages = 0;
   bool more = true;
-  // lanes 0..15 look up the row of one position each
+  // every lane looks up the row of one position (16..31 as 0..15)
   auto settle = [&]() {
     while (f.i >= f.end) {
       if (f.left == 0) {
@@ -305,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int pos = tile_pos(f.s, f.i) + (lane & 15);
     page_f = -1;
     if (visible(a, f.s, pos)) {
-      const int j = pos / a.page_size;
+      const int j = args.page_shift >= 0 ? pos >> args.page_shift : pos / a.page_size;
       in_f = pos - j * a.page_size;
       page_f = a.page_table_dev ? a.page_table_dev[f.b * a.table_stride + j] : f.b;
       if (page_f < 0 || page_f >= a.n_pages) page_f = -2;
@@ -313,68 +335,90 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
   };
   auto fetch = [&](int stage) {
     if (more) {
-      const bool bad = __any_sync(~0u, page_f == -2);
-      bad_stages = bad ? bad_stages | 1 << stage : bad_stages & ~(1 << stage);
       const int pos = tile_pos(f.s, f.i);
-      const long long ko = page_f < 0 ? -1 : page_f * a.k_page_stride + in_f * a.k_pos_stride + f.h * a.k_head_stride;
-      const long long vo = page_f < 0 ? -1 : page_f * a.v_page_stride + in_f * a.v_pos_stride + f.h * a.v_head_stride;
       const int fresh = a.k_new_dev && f.i == f.s.tiles - 1 ? f.s.n - 1 - pos : -1;   // the row of the new token
       const uint32_t dst = queue + stage * S::STAGE;
-      uint8_t* out = const_cast<uint8_t*>(queue_at) + stage * S::STAGE;
+      if (args.flat && fresh < 0 && __all_sync(~0u, page_f >= 0)) {
+        // 16 visible rows of one page
+        bad_stages &= ~(1 << stage);
+        const int in = in_f - (lane & 15);
+        const long long kstep = a.k_pos_stride * S::E, vstep = a.v_pos_stride * S::E;
+        const uint8_t* k = static_cast<const uint8_t*>(a.k_dev) +
+                           (page_f * a.k_page_stride + in * a.k_pos_stride + f.h * a.k_head_stride) * S::E + g * kstep + t * 16;
+        const uint8_t* v = static_cast<const uint8_t*>(a.v_dev) +
+                           (page_f * a.v_page_stride + in * a.v_pos_stride + f.h * a.v_head_stride) * S::E + 2 * t * vstep + g * S::VB;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const long long o = __shfl_sync(~0u, ko, g + 8 * r);
-        uint8_t* row = static_cast<uint8_t*>(a.k_dev) + (o < 0 ? 0 : o * S::E);
-        if (fresh == g + 8 * r) {
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
-          for (int j = 0; j < S::KC; ++j) {
-            constexpr int N = 16 / S::E;
-            float x[N];
-            uint32_t c[4];
-            load_row<S::IO32>(a.k_new_dev, f.b * a.new_k_seq_stride + f.h * a.new_k_head_stride + j * 4 * N + t * N, x);
-            round_row<S::KV8>(x, 1.f / a.k_scale, c);
-            const uint4 v = make_uint4(c[0], c[1], c[2], c[3]);
-            *reinterpret_cast<uint4*>(out + ((r * S::KC + j) * 32 + lane) * 16) = v;
-            if (o >= 0) *reinterpret_cast<uint4*>(row + j * 64 + t * 16) = v;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < S::KC; ++j)
-            copy_async<16>(dst + ((r * S::KC + j) * 32 + lane) * 16, row + j * 64 + t * 16, o >= 0);
+          for (int j = 0; j < S::KC; ++j) copy_async<16>(dst + ((r * S::KC + j) * 32 + lane) * 16, k + j * 64);
+          k += 8 * kstep;
         }
-      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int at = 2 * t + (r & 1) + (r >> 1) * 8;
-        const long long o = __shfl_sync(~0u, vo, at);
-        uint8_t* row = static_cast<uint8_t*>(a.v_dev) + (o < 0 ? 0 : o * S::E);
-        if (fresh == at) {
+        for (int r = 0; r < 4; ++r) {
 #pragma unroll
-          for (int c = 0; c < S::VC; ++c) {
-            constexpr int N = 16 / S::E;   // (a lane of 8 codes rounds 16 and keeps its half)
-            float x[N];
-            uint32_t code[4];
-            const int first = c * 128 / S::E + g * (S::VB / S::E);
-            load_row<S::IO32>(a.v_new_dev, f.b * a.new_v_seq_stride + f.h * a.new_v_head_stride + first / N * N, x);
-            round_row<S::KV8>(x, 1.f / a.v_scale, code);
-            uint8_t* q = out + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB;
-            if (S::VB == 16) {
-              const uint4 v = make_uint4(code[0], code[1], code[2], code[3]);
-              *reinterpret_cast<uint4*>(q) = v;
-              if (o >= 0) *reinterpret_cast<uint4*>(row + c * 128 + g * 16) = v;
-            } else {
-              const uint2 v = first % N ? make_uint2(code[2], code[3]) : make_uint2(code[0], code[1]);
-              *reinterpret_cast<uint2*>(q) = v;
-              if (o >= 0) *reinterpret_cast<uint2*>(row + g * 8) = v;
+          for (int c = 0; c < S::VC; ++c) copy_async<S::VB>(dst + v_slot(r, c), v + c * 128);
+          v += r == 1 ? 7 * vstep : vstep;
+        }
+      } else {
+        const bool bad = __any_sync(~0u, page_f == -2);
+        bad_stages = bad ? bad_stages | 1 << stage : bad_stages & ~(1 << stage);
+        const long long ko = page_f < 0 ? -1 : page_f * a.k_page_stride + in_f * a.k_pos_stride + f.h * a.k_head_stride;
+        const long long vo = page_f < 0 ? -1 : page_f * a.v_page_stride + in_f * a.v_pos_stride + f.h * a.v_head_stride;
+        uint8_t* out = const_cast<uint8_t*>(queue_at) + stage * S::STAGE;
+#pragma unroll 1
+        for (int r = 0; r < 2; ++r) {
+          const long long o = __shfl_sync(~0u, ko, g + 8 * r);
+          uint8_t* row = static_cast<uint8_t*>(a.k_dev) + (o < 0 ? 0 : o * S::E);
+          if (fresh == g + 8 * r) {
+#pragma unroll
+            for (int j = 0; j < S::KC; ++j) {
+              constexpr int N = 16 / S::E;
+              float x[N];
+              uint32_t c[4];
+              load_row<S::IO32>(a.k_new_dev, f.b * a.new_k_seq_stride + f.h * a.new_k_head_stride + j * 4 * N + t * N, x);
+              round_row<S::KV8>(x, 1.f / a.k_scale, c);
+              const uint4 v = make_uint4(c[0], c[1], c[2], c[3]);
+              *reinterpret_cast<uint4*>(out + ((r * S::KC + j) * 32 + lane) * 16) = v;
+              if (o >= 0) *reinterpret_cast<uint4*>(row + j * 64 + t * 16) = v;
             }
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int c = 0; c < S::VC; ++c)
-            copy_async<S::VB>(dst + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB, row + c * 128 + g * S::VB, o >= 0);
+            for (int j = 0; j < S::KC; ++j)
+              copy_async<16>(dst + ((r * S::KC + j) * 32 + lane) * 16, row + j * 64 + t * 16, o >= 0);
+          }
         }
+#pragma unroll 1
+        for (int r = 0; r < 4; ++r) {
+          const int at = 2 * t + (r & 1) + (r >> 1) * 8;
+          const long long o = __shfl_sync(~0u, vo, at);
+          uint8_t* row = static_cast<uint8_t*>(a.v_dev) + (o < 0 ? 0 : o * S::E);
+          if (fresh == at) {
+#pragma unroll
+            for (int c = 0; c < S::VC; ++c) {
+              constexpr int N = 16 / S::E;   // (a lane of 8 codes rounds 16 and keeps its half)
+              float x[N];
+              uint32_t code[4];
+              const int first = c * 128 / S::E + g * (S::VB / S::E);
+              load_row<S::IO32>(a.v_new_dev, f.b * a.new_v_seq_stride + f.h * a.new_v_head_stride + first / N * N, x);
+              round_row<S::KV8>(x, 1.f / a.v_scale, code);
+              uint8_t* q = out + v_slot(r, c);
+              if (S::VB == 16) {
+                const uint4 v = make_uint4(code[0], code[1], code[2], code[3]);
+                *reinterpret_cast<uint4*>(q) = v;
+                if (o >= 0) *reinterpret_cast<uint4*>(row + c * 128 + g * 16) = v;
+              } else {
+                const uint2 v = first % N ? make_uint2(code[2], code[3]) : make_uint2(code[0], code[1]);
+                *reinterpret_cast<uint2*>(q) = v;
+                if (o >= 0) *reinterpret_cast<uint2*>(row + g * 8) = v;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < S::VC; ++c) copy_async<S::VB>(dst + v_slot(r, c), row + c * 128 + g * S::VB, o >= 0);
+          }
+        }
+        if (bad && a.status_dev && lane == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
       }
-      if (bad && a.status_dev && lane == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
       f.i += kWarps;
       settle();
     }
@@ -434,72 +478,85 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     bool bad = false;
 
-    for (int i = w.i + warp; i < w.end; i += kWarps) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 1) : "memory");
-      const uint8_t* at = queue_at + stage * S::STAGE;
-      // ---- scores: positions are the columns
-      float s[2][4];
+#pragma unroll 1
+    for (int i = w.i + warp; i < w.end; i += 2 * kWarps) {
+      const bool pair = i + kWarps < w.end;
+      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
+      __syncwarp();   // V was copied by other lanes too
+      const int stage2 = stage + 1 == S::STAGES ? 0 : stage + 1;
+      // ---- scores: positions are the columns, two tiles side by side
+      float s[4][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      for (int half = 0; half < 2; ++half) {
+        const uint8_t* at = queue_at + (half ? stage2 : stage) * S::STAGE;
 #pragma unroll
-        for (int j = 0; j < S::KC; ++j) {
-          const uint4 k4 = *reinterpret_cast<const uint4*>(at + ((nt * S::KC + j) * 32 + lane) * 16);
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
-          uint32_t kb[8];
-          constexpr int NB = S::KV8 ? 8 : 4;
+        for (int n2 = 0; n2 < 2; ++n2) {
+          float(&sc)[4] = s[half * 2 + n2];
+          sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
+          if (half && !pair) continue;
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            if (S::KV8)
-              kb[2 * i2] = widen(kw[i2]), kb[2 * i2 + 1] = widen(kw[i2] >> 16);
-            else
-              kb[i2] = kw[i2];
-          }
+          for (int j = 0; j < S::KC; ++j) {
+            const uint4 k4 = *reinterpret_cast<const uint4*>(at + ((n2 * S::KC + j) * 32 + lane) * 16);
+            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+            uint32_t kb[8];
+            constexpr int NB = S::KV8 ? 8 : 4;
 #pragma unroll
-          for (int p = 0; p < NB; p += 2) {
-            const int c = j * NB + p;
-            if (S::WIDE) {
-#pragma unroll
-              for (int k = 0; k < S::QT; ++k)
-                mma(s[nt], q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[p], kb[p + 1], S::KV8);
-            } else {
-              if (S::QT > 1)
-                mma(s[nt], q[0][0][c], q[0][S::QT > 1][c], q[0][0][c + 1], q[0][S::QT > 1][c + 1], kb[p], kb[p + 1], S::KV8);
+            for (int i2 = 0; i2 < 4; ++i2) {
+              if (S::KV8)
+                kb[2 * i2] = widen(kw[i2]), kb[2 * i2 + 1] = widen_high(kw[i2]);
               else
-                mma(s[nt], q[0][0][c], 0, q[0][0][c + 1], 0, kb[p], kb[p + 1], S::KV8);
-              if (S::QT > 2) mma(s[nt], q[0][S::QT - 1][c], 0, q[0][S::QT - 1][c + 1], 0, kb[p], kb[p + 1], S::KV8);
+                kb[i2] = kw[i2];
+            }
+#pragma unroll
+            for (int p = 0; p < NB; p += 2) {
+              const int c = j * NB + p;
+              if (S::WIDE) {
+#pragma unroll
+                for (int k = 0; k < S::QT; ++k)
+                  mma(sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[p], kb[p + 1], S::KV8);
+              } else {
+                if (S::QT > 1)
+                  mma(sc, q[0][0][c], q[0][S::QT > 1][c], q[0][0][c + 1], q[0][S::QT > 1][c + 1], kb[p], kb[p + 1], S::KV8);
+                else
+                  mma(sc, q[0][0][c], 0, q[0][0][c + 1], 0, kb[p], kb[p + 1], S::KV8);
+                if (S::QT > 2) mma(sc, q[0][S::QT - 1][c], 0, q[0][S::QT - 1][c + 1], 0, kb[p], kb[p + 1], S::KV8);
+              }
             }
           }
+          if (!S::WIDE && S::QT > 1) sc[0] += sc[2], sc[1] += sc[3];
         }
-        if (!S::WIDE && S::QT > 1) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
       }
-      // ---- online softmax over the tile
-      const int pos = tile_pos(w.s, i);
-      const bool whole = pos + kTile <= w.s.n && (pos >= w.s.lo || pos + kTile <= a.sinks);
+      // ---- online softmax over the two tiles
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int pos = tile_pos(w.s, i + half * kWarps);
+        if ((half && !pair) || pos + kTile > w.s.n || (pos < w.s.lo && pos + kTile > a.sinks)) {
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if ((half && !pair) || !visible(a, w.s, pos + 8 * n2 + 2 * t + (c & 1))) s[half * 2 + n2][c] = -INFINITY;
+        }
+      }
       constexpr int NR = S::WIDE ? 2 : 1;
-      uint32_t pt[NR][S::PT][2];
+      uint32_t pt[NR][S::PT][4];
       bool grow = false;
       float fall[2];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        float top = m[r];
+        float top = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float& v = s[nt][2 * r + c];
-            if (!whole && !visible(a, w.s, pos + 8 * nt + 2 * t + c)) v = -INFINITY;
-            top = fmaxf(top, v * rs[r]);
-          }
+        for (int nt = 1; nt < 4; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        top = fmaxf(top * rs[r], m[r]);
         const float base = top == -INFINITY ? 0.f : top;
         fall[r] = ex2(m[r] - base);
         grow = grow || top != m[r];
         m[r] = top;
         float sum = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int nt = 0; nt < 4; ++nt) {
           // (the exponent is rounded once, near 0 where it counts)
           float p0 = ex2(fmaf(s[nt][2 * r], rs[r], S::SHIFT - base)), p1 = ex2(fmaf(s[nt][2 * r + 1], rs[r], S::SHIFT - base));
           sum += p0 + p1;
@@ -516,49 +573,68 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       }
       // ---- o += p v
-      auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
-        if (S::WIDE) {
 #pragma unroll
-          for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][0], pt[NR - 1][k][0], pt[0][k][1], pt[NR - 1][k][1], b0, b1, S::KV8);
+      for (int half = 0; half < 2; ++half) {
+        if (half && !pair) break;
+        const int lo = half * 2, hi = half * 2 + 1;
+        auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
+          if (S::WIDE) {
+#pragma unroll
+            for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][lo], pt[NR - 1][k][lo], pt[0][k][hi], pt[NR - 1][k][hi], b0, b1, S::KV8);
+          } else {
+            mma(c, pt[0][0][lo], pt[0][1][lo], pt[0][0][hi], pt[0][1][hi], b0, b1, S::KV8);
+            if (S::PT > 2) mma(c, pt[0][S::PT - 1][lo], 0, pt[0][S::PT - 1][hi], 0, b0, b1, S::KV8);
+          }
+        };
+        const int slot = half ? stage2 : stage;
+        if (!S::KV8) {
+          // lanes 0-7, 8-15: rows 0-7 and 8-15 of one chunk, 16-31: of the next
+          const int row = lane & 15;
+          const uint32_t base = queue + slot * S::STAGE + S::KBYTES + row * D * 2;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t b[4];
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                         : "r"(base + (((2 * j + (lane >> 4)) ^ (row & 7)) & (D / 8 - 1)) * 16)
+                         : "memory");
+            pv(o[2 * j], b[0], b[1]);
+            pv(o[2 * j + 1], b[2], b[3]);
+          }
         } else {
-          mma(c, pt[0][0][0], pt[0][1][0], pt[0][0][1], pt[0][1][1], b0, b1, S::KV8);
-          if (S::PT > 2) mma(c, pt[0][S::PT - 1][0], 0, pt[0][S::PT - 1][1], 0, b0, b1, S::KV8);
-        }
-      };
+          const uint8_t* at = queue_at + slot * S::STAGE;
+          uint32_t v[4][4];
 #pragma unroll
-      for (int c = 0; c < S::VC; ++c) {
-        uint32_t v[4][S::VB / 4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint8_t* p = at + S::KBYTES + ((r * S::VC + c) * 32 + lane) * S::VB;
-          if (S::VB == 16) {
-            const uint4 u = *reinterpret_cast<const uint4*>(p);
-            v[r][0] = u.x, v[r][1] = u.y, v[r][S::VB / 4 - 2] = u.z, v[r][S::VB / 4 - 1] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            v[r][0] = u.x, v[r][1] = u.y;
-          }
-        }
-#pragma unroll
-        for (int i2 = 0; i2 < S::VB / 4; ++i2) {
-          if (S::KV8) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              // codes of two positions side by side, two dims in a register
-              const uint32_t e = __byte_perm(v[0][i2], v[1][i2], half ? 0x7362 : 0x5140);
-              const uint32_t d = __byte_perm(v[2][i2], v[3][i2], half ? 0x7362 : 0x5140);
-              pv(o[i2 * 4 + half * 2], widen(e), widen(d));
-              pv(o[i2 * 4 + half * 2 + 1], widen(e >> 16), widen(d >> 16));
+          for (int r = 0; r < 4; ++r) {
+            const uint8_t* p = at + v_slot(r, 0);
+            if (S::VB == 16) {
+              const uint4 u = *reinterpret_cast<const uint4*>(p);
+              v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+            } else {
+              const uint2 u = *reinterpret_cast<const uint2*>(p);
+              v[r][0] = u.x, v[r][1] = u.y;
             }
-          } else {
-            pv(o[c * 8 + i2 * 2], __byte_perm(v[0][i2], v[1][i2], 0x5410), __byte_perm(v[2][i2], v[3][i2], 0x5410));
-            pv(o[c * 8 + i2 * 2 + 1], __byte_perm(v[0][i2], v[1][i2], 0x7632), __byte_perm(v[2][i2], v[3][i2], 0x7632));
           }
+#pragma unroll
+          for (int i2 = 0; i2 < S::VB / 4; ++i2)
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              // codes of two positions side by side, two dims in a register
+              const uint32_t e = __byte_perm(v[0][i2], v[1][i2], h2 ? 0x7362 : 0x5140);
+              const uint32_t d = __byte_perm(v[2][i2], v[3][i2], h2 ? 0x7362 : 0x5140);
+              pv(o[i2 * 4 + h2 * 2], widen(e), widen(d));
+              pv(o[i2 * 4 + h2 * 2 + 1], widen_high(e), widen_high(d));
+            }
         }
       }
-      bad = bad || (bad_stages >> stage & 1);
+      bad = bad || (bad_stages >> stage & 1) || (pair && bad_stages >> stage2 & 1);
+      __syncwarp();   // all lanes have read what is overwritten
       fetch(stage);
-      stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+      stage = stage2;
+      if (pair) {
+        fetch(stage);
+        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+      }
     }
 
     // ---- the warps' results joined
@@ -582,23 +658,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         float top = -INFINITY;
         for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[k * S::ROWS + head]);
         const float e = top == -INFINITY ? 0.f : ex2(m[r] - top);
-        // a lane's accumulators are 2 runs of consecutive dims for each V chunk
-        constexpr int RUN = S::VB / S::E;
         float* row = merge + (warp * S::ROWS + head) * D;
-#pragma unroll
-        for (int c = 0; c < S::VC; ++c)
+        const auto value = [&](int i, int half) {
+          const float* acc = o[i];
+          return (S::WIDE ? acc[2 * r + half] : acc[half] + acc[2 + half]) * e;
+        };
+        if (S::KV8) {   // a lane's accumulators are two runs of D / 8 consecutive dims
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int i = 0; i < RUN; i += 4) {
-              float v[4];
+            for (int i = 0; i < D / 8; i += 4)
+              *reinterpret_cast<float4*>(row + (2 * t + half) * (D / 8) + i) =
+                  make_float4(value(i, half), value(i + 1, half), value(i + 2, half), value(i + 3, half));
+        } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float* acc = o[c * RUN + i + k];
-                v[k] = (S::WIDE ? acc[2 * r + half] : acc[half] + acc[2 + half]) * e;
-              }
-              *reinterpret_cast<float4*>(row + c * 8 * RUN + (2 * t + half) * RUN + i) = make_float4(v[0], v[1], v[2], v[3]);
-            }
+          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(row + i * 8 + 2 * t) = make_float2(value(i, 0), value(i, 1));
+        }
       }
     }
     __syncthreads();
@@ -784,6 +859,8 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   if (a->n_seqs == 0) return XLPK_OK;
   Args args;
   args.a = *a;
+  args.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz(a->page_size) : -1;
+  args.flat = a->page_size % kTile == 0;
   args.joins = static_cast<int4*>(workspace_dev);
   args.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + kJoinBytes);
   const int ctas = std::min(sms, kMaxCtas);
