@@ -19,17 +19,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 256;
+constexpr int kJoinWarps = 8;
+constexpr int kThreads = kJoinWarps * 32;   // of the join
+constexpr int kMaxCtas = 160;
+constexpr int kPieces = 16;
 constexpr int kTile = 16;   // positions of a tile; a warp takes two of its tiles at a time
 
 struct Args {
   xlpk_attention_args a;
-  float* parts;     // [CTAs][2] slots of partial results
+  float* parts;     // [workers][2] slots of partial results
+  int ctas;         // of the attention
   int page_shift;   // log2 of page_size, or -1
   bool flat;        // a tile never crosses a page
-  int4* joins;      // [CTAs] (sequence, kv head, last CTA, -) of the segment that CTA begins and another ends; .x < 0: none
+  int4* joins;      // [workers] (sequence, kv head, last worker, -) of the segment that a worker begins and another ends; .x < 0: none
+  int* team;        // warps of a worker
 };
 
 // The tiles of one sequence: those that hold a visible position.
@@ -59,13 +62,12 @@ __device__ inline bool visible(const xlpk_attention_args& a, const Seq& s, int t
 // at segment borders: a segment is one kv head of one sequence.
 struct Walk {
   int b, h, i, end;      // tiles [i, end) of segment (b, h)
-  long long left;        // tiles after them
+  int left;              // tiles after them
   Seq s;
 };
-__device__ inline void walk_cut(Walk& w, long long n) {
-  const long long e = w.i + n;
-  w.end = e < w.s.tiles ? static_cast<int>(e) : w.s.tiles;
-  w.left = e - w.end;
+__device__ inline void walk_cut(Walk& w, int n) {
+  w.end = w.i + min(n, w.s.tiles - w.i);
+  w.left = n - (w.end - w.i);
 }
 // To the next segment (left > 0).
 __device__ inline void walk_next(const xlpk_attention_args& a, Walk& w) {
@@ -78,12 +80,26 @@ __device__ inline void walk_next(const xlpk_attention_args& a, Walk& w) {
   walk_cut(w, w.left);
 }
 
+// `total` tiles over `workers`, the first `more` of which take one more than the others.
+struct Shares {
+  unsigned each, more;
+  __device__ Shares(unsigned total, unsigned workers) : each(total / workers), more(total - each * workers) {}
+  __device__ int first(int worker) const { return worker * each + min(static_cast<unsigned>(worker), more); }
+  __device__ int owner(unsigned tile) const {
+    const unsigned split = more * (each + 1);
+    return tile < split ? tile / (each + 1) : more + (tile - split) / each;
+  }
+};
+
 template <int D_, bool KV8_, bool WIDE_, bool IO32_>
 struct Shape {
   static constexpr int D = D_;
   static constexpr bool KV8 = KV8_;      // e4m3 cache, fp16 operands; else bf16
   static constexpr bool WIDE = WIDE_;    // 9 to 16 query heads per kv head; else up to 8
   static constexpr bool IO32 = IO32_;
+  // e4m3 tiles are half the bytes for the same work: more warps, as far as registers and queue go
+  // (four sequences of 131072, d 128: 8 warps 255 us, 12 245, 16 411; 16 of 8192, d 64: 57, 53, 49)
+  static constexpr int WARPS = WIDE || !KV8 ? 8 : D == 128 ? 12 : 16, THREADS = WARPS * 32;
   static constexpr int E = KV8 ? 1 : 2;
   static constexpr int ROWS = WIDE ? 16 : 8;
   // what one lane copies of a cache row: a K row is read by the 4 lanes of a quad in 16-byte
@@ -92,10 +108,11 @@ struct Shape {
   static constexpr int VB = D * E / 8 >= 16 ? 16 : 8;
   static constexpr int VC = D * E / 8 / VB;
   static constexpr int KBYTES = 2 * KC * 512, STAGE = KBYTES + 4 * VC * VB * 32;
-  static constexpr int MERGE = kWarps * ROWS * (D + 2) * 4;
-  static constexpr int FIT = (232448 - 1024 - MERGE) / (STAGE * kWarps);
+  static constexpr int MERGE = WARPS * ROWS * (D + 2) * 4;
+  static constexpr int FIT = (232448 - 1024 - MERGE) / (STAGE * WARPS);
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr int SMEM = STAGES * STAGE * kWarps + MERGE;
+  static constexpr int SMEM = STAGES * STAGE * WARPS + MERGE;
+  static_assert(STAGES >= 2, "a step takes two tiles");
   static constexpr int QT = IO32 ? (KV8 ? 2 : 3) : 1;   // terms of q
   static constexpr int PT = IO32 && !KV8 ? 3 : 2;       // terms of p
   static constexpr int QR = D / 8;                      // registers of one term of one row
@@ -224,66 +241,90 @@ __device__ inline float ex2(float x) {
 __device__ inline float lse_of(float m, float l, int shift) { return l == 0 ? -INFINITY : (m - shift) * kLn2 + logf(l); }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Args args) {
+__global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_constant__ Args args) {
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up meanwhile; it waits for this grid's end
-  __shared__ long long scan[kWarps], start[2];
+  __shared__ int scan[S::WARPS], most[S::WARPS], start[S::WARPS][2];
   const xlpk_attention_args& a = args.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int group = a.n_q_heads / a.n_kv_heads;
   constexpr int D = S::D;
 
-  // ---- this CTA's even share [x0, x1) of all tiles, and the segment it begins in
+  // ---- the worker's even share [x0, x0 + count) of all tiles, and the segment it begins in.
+  // A worker is a CTA whose warps take a segment's tiles in turn, or, where that cuts no segment into
+  // more than about kPieces, a warp: then a short segment costs no barrier and no idle warps
+  // (64 sequences of 100 positions 19.6 us with CTAs, 15.1 with warps; one long sequence cut
+  // into 1184 pieces would spend more in the join).
   Walk w{};
-  long long count;   // its tiles
-  int ctas;          // CTAs that have any
-  long long tiles_in_all;
-  long long x0;
+  int count, x0;
+  Shares shares(1, 1);
+  int worker, workers, team;
   {
-    const int per = (a.n_seqs + kThreads - 1) / kThreads, b0 = min(static_cast<int>(threadIdx.x) * per, a.n_seqs),
+    const int per = (a.n_seqs + S::THREADS - 1) / S::THREADS, b0 = min(static_cast<int>(threadIdx.x) * per, a.n_seqs),
               b1 = min(b0 + per, a.n_seqs);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_of(a, b).tiles;
-    long long sum = mine;
+    int mine = 0, longest = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int n = seq_of(a, b).tiles;
+      mine += n;
+      longest = max(longest, n);
+    }
+    longest = __reduce_max_sync(~0u, longest);
+    int sum = mine;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(~0u, sum, o);
+      const int y = __shfl_up_sync(~0u, sum, o);
       if (lane >= o) sum += y;
     }
-    if (lane == 31) scan[warp] = sum;
+    if (lane == 31) scan[warp] = sum, most[warp] = longest;
     __syncthreads();
-    long long total = 0, before = sum - mine;
-    for (int i = 0; i < kWarps; ++i) {
+    int total = 0, before = sum - mine;
+#pragma unroll 1
+    for (int i = 0; i < S::WARPS; ++i) {
       if (i < warp) before += scan[i];
       total += scan[i];
+      longest = max(longest, most[i]);
     }
     total *= a.n_kv_heads;
-    tiles_in_all = total;
-    ctas = total < gridDim.x ? static_cast<int>(total) : gridDim.x;
-    const bool any = static_cast<int>(blockIdx.x) < ctas;
-    x0 = any ? blockIdx.x * total / ctas : 0;
-    count = any ? (blockIdx.x + 1) * total / ctas - x0 : 0;
-    if (any && mine > 0 && before * a.n_kv_heads <= x0 && x0 < (before + mine) * a.n_kv_heads) {
-      int b = b0;
-      long long off = x0 - before * a.n_kv_heads;
-      for (;; ++b) {
-        const long long seg = static_cast<long long>(seq_of(a, b).tiles) * a.n_kv_heads;
-        if (off < seg) break;
-        off -= seg;
+    const int warps = gridDim.x * S::WARPS;
+    team = static_cast<long long>(longest) * warps <= static_cast<long long>(kPieces) * total ? 1 : S::WARPS;
+    const int all = team == 1 ? warps : gridDim.x;
+    worker = team == 1 ? blockIdx.x * S::WARPS + warp : blockIdx.x;
+    workers = min(total, all);
+    if (workers > 0) shares = Shares(total, workers);
+    if (mine > 0)
+#pragma unroll 1
+      for (int i = 0; i < S::WARPS / team; ++i) {
+        const int wk = blockIdx.x * (S::WARPS / team) + i;
+        if (wk >= workers) break;
+        const int x = shares.first(wk);
+        if (x < before * a.n_kv_heads || x >= (before + mine) * a.n_kv_heads) continue;
+        int b = b0;
+        int off = x - before * a.n_kv_heads;
+        for (;; ++b) {
+          const int seg = seq_of(a, b).tiles * a.n_kv_heads;
+          if (off < seg) break;
+          off -= seg;
+        }
+        start[i][0] = b;
+        start[i][1] = off;
       }
-      start[0] = b;
-      start[1] = off;
-    }
-    // who joins the pieces of the segment that this CTA begins and does not end is said at its end
-    if (threadIdx.x == 0) args.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    // who joins the pieces of the segment that this worker begins and does not end is said at its end
+    if (lane == 0 && (team == 1 || warp == 0)) args.joins[worker] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *args.team = team;
     __syncthreads();
+    const bool any = worker < workers;
+    x0 = any ? shares.first(worker) : 0;
+    count = any ? shares.first(worker + 1) - x0 : 0;
     if (any) {
-      w.b = static_cast<int>(start[0]);
+      const int* at = start[team == 1 ? warp : 0];
+      w.b = at[0];
       w.s = seq_of(a, w.b);
-      w.h = static_cast<int>(start[1] / w.s.tiles);
-      w.i = static_cast<int>(start[1] - static_cast<long long>(w.h) * w.s.tiles);
+      w.h = static_cast<unsigned>(at[1]) / static_cast<unsigned>(w.s.tiles);
+      w.i = at[1] - w.h * w.s.tiles;
       walk_cut(w, count);
     }
   }
+  const int lead = team == 1 ? warp : 0, rank = warp - lead;   // the worker's first warp, and this one's place in it
 
   // ---- rows without positions
   for (int b = blockIdx.x; b < a.n_seqs; b += gridDim.x) {
@@ -291,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const bool bad = n < 0 || n > static_cast<long long>(a.table_cols) * a.page_size;
     if (n != 0 && !bad) continue;
     const float v = bad ? __int_as_float(0x7fffffff) : 0.f;
-    for (int i = threadIdx.x * 4; i < a.n_q_heads * D; i += kThreads * 4)
+    for (int i = threadIdx.x * 4; i < a.n_q_heads * D; i += S::THREADS * 4)
       store_out<S::IO32>(a.out_dev, b * a.out_seq_stride + i / D * a.out_head_stride + i % D, make_float4(v, v, v, v));
     if (a.lse_dev)
-      for (int i = threadIdx.x; i < a.n_q_heads; i += kThreads)
+      for (int i = threadIdx.x; i < a.n_q_heads; i += S::THREADS)
         a.lse_dev[static_cast<long long>(b) * a.n_q_heads + i] = bad ? v : -INFINITY;
     if (bad && a.status_dev && threadIdx.x == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
   }
@@ -311,26 +352,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     return S::KBYTES + row * D * 2 + (((c * 8 + g) ^ (row & 7)) & (D / 8 - 1)) * 16;
   };
   Walk f = w;            // the tile that is fetched next
-  f.i += warp;
-  int page_f = -1, in_f = 0, bad_stages = 0;
+  f.i += rank;
+  int bad_stages = 0;
   bool more = true;
-  // every lane looks up the row of one position (16..31 as 0..15)
-  auto settle = [&]() {
+  // Pages are looked up ahead of the copies that need them.  Where a tile never crosses a page,
+  // lane i holds the page of the i-th of the segment's next 32 tiles of this warp, and `later` those
+  // of the 32 after them; otherwise every lane holds the page of one position of the next tile
+  // (16..31 as 0..15).  -1: not visible, -2: outside the pool.
+  int pages = -1, later = -1, used = 0;
+  const auto page_of = [&](int pos) {
+    const int j = args.page_shift >= 0 ? pos >> args.page_shift : pos / a.page_size;
+    const int page = a.page_table_dev ? a.page_table_dev[f.b * a.table_stride + j] : f.b;
+    return page < 0 || page >= a.n_pages ? -2 : page;
+  };
+  const auto in_page = [&](int pos) { return args.page_shift >= 0 ? pos & (a.page_size - 1) : pos % a.page_size; };
+  const auto batch = [&](int i) { return i < f.end ? page_of(min(tile_pos(f.s, i), f.s.n - 1)) : -1; };
+  const auto settle = [&](bool fresh) {   // to the next tile; `fresh`: of a segment that is new
     while (f.i >= f.end) {
       if (f.left == 0) {
         more = false;
         return;
       }
       walk_next(a, f);
-      f.i += warp;
+      f.i += rank;
+      fresh = true;
     }
-    const int pos = tile_pos(f.s, f.i) + (lane & 15);
-    page_f = -1;
-    if (visible(a, f.s, pos)) {
-      const int j = args.page_shift >= 0 ? pos >> args.page_shift : pos / a.page_size;
-      in_f = pos - j * a.page_size;
-      page_f = a.page_table_dev ? a.page_table_dev[f.b * a.table_stride + j] : f.b;
-      if (page_f < 0 || page_f >= a.n_pages) page_f = -2;
+    if (!args.flat) {
+      const int pos = tile_pos(f.s, f.i) + (lane & 15);
+      pages = visible(a, f.s, pos) ? page_of(pos) : -1;
+    } else if (fresh) {
+      pages = batch(f.i + lane * team);
+      later = batch(f.i + (lane + 32) * team);
+      used = 0;
+    } else if (++used == 32) {
+      pages = later;
+      later = batch(f.i + (lane + 32) * team);
+      used = 0;
     }
   };
   auto fetch = [&](int stage) {
@@ -338,15 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       const int pos = tile_pos(f.s, f.i);
       const int fresh = a.k_new_dev && f.i == f.s.tiles - 1 ? f.s.n - 1 - pos : -1;   // the row of the new token
       const uint32_t dst = queue + stage * S::STAGE;
-      if (args.flat && fresh < 0 && __all_sync(~0u, page_f >= 0)) {
+      const int page = args.flat ? __shfl_sync(~0u, pages, used) : -1;
+      if (page >= 0 && fresh < 0 && pos + kTile <= f.s.n && (pos >= f.s.lo || pos + kTile <= a.sinks)) {
         // 16 visible rows of one page
         bad_stages &= ~(1 << stage);
-        const int in = in_f - (lane & 15);
+        const int in = in_page(pos);
         const long long kstep = a.k_pos_stride * S::E, vstep = a.v_pos_stride * S::E;
         const uint8_t* k = static_cast<const uint8_t*>(a.k_dev) +
-                           (page_f * a.k_page_stride + in * a.k_pos_stride + f.h * a.k_head_stride) * S::E + g * kstep + t * 16;
+                           (page * a.k_page_stride + in * a.k_pos_stride + f.h * a.k_head_stride) * S::E + g * kstep + t * 16;
         const uint8_t* v = static_cast<const uint8_t*>(a.v_dev) +
-                           (page_f * a.v_page_stride + in * a.v_pos_stride + f.h * a.v_head_stride) * S::E + 2 * t * vstep + g * S::VB;
+                           (page * a.v_page_stride + in * a.v_pos_stride + f.h * a.v_head_stride) * S::E + 2 * t * vstep + g * S::VB;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
@@ -360,6 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
           v += r == 1 ? 7 * vstep : vstep;
         }
       } else {
+        const int at = pos + (lane & 15), in_f = in_page(at),
+                  page_f = !args.flat ? pages : visible(a, f.s, at) ? page : -1;
         const bool bad = __any_sync(~0u, page_f == -2);
         bad_stages = bad ? bad_stages | 1 << stage : bad_stages & ~(1 << stage);
         const long long ko = page_f < 0 ? -1 : page_f * a.k_page_stride + in_f * a.k_pos_stride + f.h * a.k_head_stride;
@@ -419,20 +479,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         if (bad && a.status_dev && lane == 0) *a.status_dev = XLPK_ERR_INVALID_ARG;
       }
-      f.i += kWarps;
-      settle();
+      f.i += team;
+      settle(false);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  settle();
+  settle(true);
 #pragma unroll 1
   for (int i = 0; i < S::STAGES; ++i) fetch(i);
 
-  float* const merge = reinterpret_cast<float*>(smem + S::STAGES * S::STAGE * kWarps);
-  float* const merge_m = merge + kWarps * S::ROWS * D;
-  float* const merge_l = merge_m + kWarps * S::ROWS;
+  float* const merge = reinterpret_cast<float*>(smem + S::STAGES * S::STAGE * S::WARPS);
+  float* const merge_m = merge + S::WARPS * S::ROWS * D;
+  float* const merge_l = merge_m + S::WARPS * S::ROWS;
+  const auto worker_sync = [&]() {
+    if (team == 1) __syncwarp();
+    else __syncthreads();
+  };
   const float s2 = a.scale * kLog2e * (S::KV8 ? a.k_scale : 1.f);
-  long long x = x0;   // the segment's first tile here
+  int x = x0;   // the segment's first tile here
   int stage = 0;
   for (;;) {
     // ---- q of the segment's heads, as terms
@@ -479,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     bool bad = false;
 
 #pragma unroll 1
-    for (int i = w.i + warp; i < w.end; i += 2 * kWarps) {
-      const bool pair = i + kWarps < w.end;
+    for (int i = w.i + rank; i < w.end; i += 2 * team) {
+      const bool pair = i + team < w.end;
       asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
       __syncwarp();   // V was copied by other lanes too
       const int stage2 = stage + 1 == S::STAGES ? 0 : stage + 1;
@@ -529,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
       // ---- online softmax over the two tiles
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int pos = tile_pos(w.s, i + half * kWarps);
+        const int pos = tile_pos(w.s, i + half * team);
         if ((half && !pair) || pos + kTile > w.s.n || (pos < w.s.lo && pos + kTile > a.sinks)) {
 #pragma unroll
           for (int n2 = 0; n2 < 2; ++n2)
@@ -638,25 +702,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
 
     // ---- the warps' results joined
-    const int active = min(w.end - w.i, kWarps);
+    const int active = min(w.end - w.i, team);
 #pragma unroll
     for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
       if (bad) l[r] = __int_as_float(0x7fffffff);
-      if (t == 0 && warp < active) {
+      if (t == 0 && rank < active) {
         merge_m[warp * S::ROWS + g + 8 * r] = m[r];
         merge_l[warp * S::ROWS + g + 8 * r] = l[r];
       }
     }
-    __syncthreads();
-    if (warp < active) {
+    worker_sync();
+    if (rank < active) {
 #pragma unroll
       for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
         const int head = g + 8 * r;
         if (head >= group) continue;
         float top = -INFINITY;
-        for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[k * S::ROWS + head]);
+        for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[(lead + k) * S::ROWS + head]);
         const float e = top == -INFINITY ? 0.f : ex2(m[r] - top);
         float* row = merge + (warp * S::ROWS + head) * D;
         const auto value = [&](int i, int half) {
@@ -676,18 +740,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
       }
     }
-    __syncthreads();
+    worker_sync();
     const bool begins = w.i == 0, ends = w.end == w.s.tiles;
-    float* slot = args.parts + (blockIdx.x * 2ll + begins) * S::SLOT;
-    for (int i = threadIdx.x * 4; i < group * D; i += kThreads * 4) {
+    float* slot = args.parts + (worker * 2ll + begins) * S::SLOT;
+    for (int i = (rank * 32 + lane) * 4; i < group * D; i += team * 128) {
       const int head = i / D, d = i % D;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float top = -INFINITY, den = 0.f;
-      for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[k * S::ROWS + head]);
+      for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[(lead + k) * S::ROWS + head]);
       for (int k = 0; k < active; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(merge + (k * S::ROWS + head) * D + d);
+        const float4 v = *reinterpret_cast<const float4*>(merge + ((lead + k) * S::ROWS + head) * D + d);
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        den += merge_l[k * S::ROWS + head] * (top == -INFINITY ? 0.f : ex2(merge_m[k * S::ROWS + head] - top));
+        den += merge_l[(lead + k) * S::ROWS + head] * (top == -INFINITY ? 0.f : ex2(merge_m[(lead + k) * S::ROWS + head] - top));
       }
       if (begins && ends) {
         const float f = den == 0 ? 0.f : (S::KV8 ? a.v_scale : 1.f) / den;
@@ -700,63 +764,83 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         if (d == 0) slot[S::ROWS * D + head] = top, slot[S::ROWS * (D + 1) + head] = den;
       }
     }
-    if (begins && !ends && threadIdx.x == 0) {
-      // the CTA that holds the segment's last tile: the largest c with c * total / ctas <= it
-      const long long last = x + w.s.tiles - 1;
-      args.joins[blockIdx.x] = make_int4(w.b, w.h, static_cast<int>(((last + 1) * ctas - 1) / tiles_in_all), 0);
+    if (begins && !ends && rank == 0 && lane == 0) {
+      args.joins[worker] = make_int4(w.b, w.h, shares.owner(x + w.s.tiles - 1), 0);
     }
+    if (team == 1) __syncwarp();   // the scratch has been read
     x += w.end - w.i;
     if (w.left == 0) break;
     walk_next(a, w);
   }
 }
 
-// One CTA per (CTA that begins a segment which another ends, query head of the group):
-// the pieces of the segment joined by their maxima.
+template <class S>
+__device__ inline void store_joined(const xlpk_attention_args& a, const int4& j, int head, int d, float4 sum, float top, float den) {
+  const float f = den == 0 ? 0.f : (S::KV8 ? a.v_scale : 1.f) / den;
+  const int h = j.y * (a.n_q_heads / a.n_kv_heads) + head;
+  store_out<S::IO32>(a.out_dev, j.x * a.out_seq_stride + h * a.out_head_stride + d,
+                     make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+  if (d == 0 && a.lse_dev) a.lse_dev[static_cast<long long>(j.x) * a.n_q_heads + h] = lse_of(top, den, S::SHIFT);
+}
+
+// The pieces of every segment that one worker begins and another ends, joined by their maxima:
+// for each query head of the group by one CTA (workers that are CTAs: few segments, up to
+// one piece for each SM) or by one warp (many segments of few pieces).
 template <class S>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args args) {
-  constexpr int D = S::D, TEAMS = kThreads / D;
-  __shared__ float factor[kMaxCtas], sums[TEAMS][D], red[2 * kWarps];
+  constexpr int D = S::D, LANES = D / 4, TEAMS = kThreads / LANES;
+  __shared__ float4 sums[TEAMS][LANES];
+  __shared__ float dens[TEAMS], tops[kJoinWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const xlpk_attention_args& a = args.a;
-  const int4 j = args.joins[blockIdx.x];
+  const int group = a.n_q_heads / a.n_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool by_warp = *args.team == 1;
+  const int item = by_warp ? blockIdx.x * kJoinWarps + warp : blockIdx.x, head = item % group, worker = item / group;
+  if (worker >= args.ctas * (by_warp ? S::WARPS : 1)) return;
+  const int4 j = args.joins[worker];
   if (j.x < 0) return;
-  const int head = blockIdx.y, group = a.n_q_heads / a.n_kv_heads, n = j.z - blockIdx.x + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // piece 0 is the slot of the segment that its CTA begins, the others continue theirs
-  auto slot = [&](int k) { return args.parts + ((blockIdx.x + k) * 2ll + (k == 0)) * S::SLOT; };
+  const int n = j.z - worker + 1;
+  // piece 0 is the slot of the segment that its worker begins, the others continue theirs
+  const auto slot = [&](int k) { return args.parts + ((worker + k) * 2ll + (k == 0)) * S::SLOT; };
+  const int size = by_warp ? 32 : kThreads, me = by_warp ? lane : threadIdx.x, teams = size / LANES;
   float top = -INFINITY;
-  for (int k = threadIdx.x; k < n; k += kThreads) top = fmaxf(top, factor[k] = slot(k)[S::ROWS * D + head]);
+  for (int k = me; k < n; k += size) top = fmaxf(top, slot(k)[S::ROWS * D + head]);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-  for (int k = 0; k < kWarps; ++k) top = fmaxf(top, red[k]);
-  float den = 0.f;
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    const float e = top == -INFINITY ? 0.f : ex2(factor[k] - top);
-    factor[k] = e;
-    den += e * slot(k)[S::ROWS * (D + 1) + head];
+  if (!by_warp) {
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    for (int k = 0; k < kJoinWarps; ++k) top = fmaxf(top, tops[k]);
   }
-  for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(~0u, den, o);
-  if (lane == 0) red[kWarps + warp] = den;
-  __syncthreads();
-  den = 0.f;
-  for (int k = 0; k < kWarps; ++k) den += red[kWarps + k];
-  const int d = threadIdx.x % D, team = threadIdx.x / D;
-  float sum = 0.f;
-#pragma unroll 8
-  for (int k = team; k < n; k += TEAMS) sum += factor[k] * slot(k)[head * D + d];
-  sums[team][d] = sum;
-  __syncthreads();
-  if (team != 0) return;
-  for (int k = 1; k < TEAMS; ++k) sum += sums[k][d];
-  const float v = den == 0 ? 0.f : sum * (S::KV8 ? a.v_scale : 1.f) / den;
-  const long long at = j.x * a.out_seq_stride + (j.y * group + head) * a.out_head_stride + d;
-  if (S::IO32)
-    static_cast<float*>(a.out_dev)[at] = v;
-  else
-    static_cast<__nv_bfloat16*>(a.out_dev)[at] = __float2bfloat16_rn(v);
-  if (d == 0 && a.lse_dev) a.lse_dev[static_cast<long long>(j.x) * a.n_q_heads + j.y * group + head] = lse_of(top, den, S::SHIFT);
+  const int d = me % LANES, team = me / LANES;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+#pragma unroll 4
+  for (int k = team; k < n; k += teams) {
+    const float* p = slot(k);
+    const float4 v = *reinterpret_cast<const float4*>(p + head * D + d * 4);
+    const float e = top == -INFINITY ? 0.f : ex2(p[S::ROWS * D + head] - top);
+    sum.x += e * v.x, sum.y += e * v.y, sum.z += e * v.z, sum.w += e * v.w;
+    den += e * p[S::ROWS * (D + 1) + head];
+  }
+  if (!by_warp) {
+    sums[team][d] = sum;
+    if (d == 0) dens[team] = den;
+    __syncthreads();
+    if (team != 0) return;
+    for (int k = 1; k < TEAMS; ++k) {
+      const float4 v = sums[k][d];
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+      den += dens[k];
+    }
+  } else if (LANES < 32) {
+    for (int o = LANES; o < 32; o <<= 1) {
+      sum.x += __shfl_xor_sync(~0u, sum.x, o), sum.y += __shfl_xor_sync(~0u, sum.y, o);
+      sum.z += __shfl_xor_sync(~0u, sum.z, o), sum.w += __shfl_xor_sync(~0u, sum.w, o);
+      den += __shfl_xor_sync(~0u, den, o);
+    }
+    if (team != 0) return;
+  }
+  store_joined<S>(a, j, head, d * 4, sum, top, den);
 }
 
 bool power_of_two_scale(float s) {
@@ -786,6 +870,9 @@ xlpk_status check_args(const xlpk_attention_args* a) {
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: scale is not finite and positive");
   if (a->kv_dtype == XLPK_DTYPE_FP8_E4M3 && (!power_of_two_scale(a->k_scale) || !power_of_two_scale(a->v_scale)))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: cache scales are powers of two in [2^-24, 2^24]");
+  if (static_cast<int64_t>(a->n_seqs) * a->n_kv_heads >
+      INT32_MAX / (static_cast<int64_t>(a->table_cols) * a->page_size / kTile + 2))
+    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: n_seqs * n_kv_heads * capacity of 16 * 2^31 or more");
   if (a->n_seqs == 0) return XLPK_OK;
   if (!a->q_dev || !a->seq_lens_dev || !a->out_dev || (!a->k_new_dev) != (!a->v_new_dev) ||
       ((!a->k_dev || !a->v_dev) && a->n_pages > 0))
@@ -815,9 +902,10 @@ xlpk_status launch(const Args& args, int ctas, cudaStream_t st) {
     XLPK_CUDA(cudaFuncSetAttribute(attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  attention_kernel<S><<<ctas, kThreads, S::SMEM, st>>>(args);
+  attention_kernel<S><<<ctas, S::THREADS, S::SMEM, st>>>(args);
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(ctas, args.a.n_q_heads / args.a.n_kv_heads);
+  const int group = args.a.n_q_heads / args.a.n_kv_heads;
+  c.gridDim = dim3(std::max(ctas * group, (ctas * S::WARPS * group + kJoinWarps - 1) / kJoinWarps));
   c.blockDim = dim3(kThreads);
   c.stream = st;
   cudaLaunchAttribute early{};
@@ -837,14 +925,15 @@ xlpk_status launch_for(const Args& args, int ctas, cudaStream_t st) {
   return io32 ? launch<Shape<D, KV8, false, true>>(args, ctas, st) : launch<Shape<D, KV8, false, false>>(args, ctas, st);
 }
 
-constexpr int64_t kJoinBytes = kMaxCtas * sizeof(int4);
+constexpr int kMaxWorkers = kMaxCtas * 16;
+constexpr int64_t kJoinBytes = (kMaxWorkers + 1) * sizeof(int4);
 
 }  // namespace
 
 extern "C" int64_t xlpk_decode_attention_workspace(const xlpk_attention_args* a) {
   if (!shape_ok(a)) return 0;
-  const int64_t rows = a->n_q_heads / a->n_kv_heads > 8 ? 16 : 8;
-  return kJoinBytes + kMaxCtas * 2 * rows * (static_cast<int64_t>(a->head_dim) + 2) * 4;
+  // (16 warps of 8 rows, or 8 of 16)
+  return kJoinBytes + kMaxWorkers * 2 * 8 * (static_cast<int64_t>(a->head_dim) + 2) * 4;
 }
 
 extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void* workspace_dev, int64_t workspace_bytes,
@@ -861,9 +950,11 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   args.a = *a;
   args.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz(a->page_size) : -1;
   args.flat = a->page_size % kTile == 0;
+  args.ctas = std::min(sms, kMaxCtas);
   args.joins = static_cast<int4*>(workspace_dev);
+  args.team = reinterpret_cast<int*>(args.joins + kMaxWorkers);
   args.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + kJoinBytes);
-  const int ctas = std::min(sms, kMaxCtas);
+  const int ctas = args.ctas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (a->head_dim == 64)
     return a->kv_dtype == XLPK_DTYPE_BF16 ? launch_for<64, false>(args, ctas, st) : launch_for<64, true>(args, ctas, st);
