@@ -22,7 +22,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinWarps = 8;
 constexpr int kThreads = kJoinWarps * 32;   // of the join
 constexpr int kMaxCtas = 160;
-constexpr int kPieces = 16;
+constexpr int kPieces = 4;
 constexpr int kTile = 16;   // positions of a tile; a warp takes two of its tiles at a time
 
 struct Args {
@@ -252,9 +252,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
 
   // ---- the worker's even share [x0, x0 + count) of all tiles, and the segment it begins in.
   // A worker is a CTA whose warps take a segment's tiles in turn, or, where that cuts no segment into
-  // more than about kPieces, a warp: then a short segment costs no barrier and no idle warps
-  // (64 sequences of 100 positions 19.6 us with CTAs, 15.1 with warps; one long sequence cut
-  // into 1184 pieces would spend more in the join).
+  // more than about kPieces, a warp: then a short segment costs no barrier and no idle warps (64
+  // sequences of 1024, 8 kv heads: 35 us against 38 with CTAs).  Longer segments lose by it: their
+  // pieces go through memory (64 behind a 4096 window: 101 us against 95).
   Walk w{};
   int count, x0;
   Shares shares(1, 1);

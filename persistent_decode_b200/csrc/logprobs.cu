@@ -17,11 +17,11 @@ namespace {
 constexpr int kMaxTop = 64;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kGroups = 128;       // most groups of threads, each known by its largest logit
-constexpr int kMarks = 64;         // stretches of rounds that a warp knows the largest logit of
+constexpr int kMarks = 32;         // stretches of rounds that a thread knows its largest logit of
 constexpr int kUnroll = 4;         // 16-byte vectors a thread takes in a round
-constexpr int kStages = 3;         // rounds on their way
+constexpr int kStages = 2;         // rounds on their way
 constexpr int kStep = kUnroll * kThreads;
 constexpr int kPushed = 512;       // candidates that are ranked at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -152,7 +152,7 @@ constexpr int kQueueBytes = kStages * kStep * 16;
 struct alignas(16) Shared {
   unsigned long long pushed[kMaxCluster * kMaxTop];
   unsigned long long lists[kMaxCluster][kMaxTop];   // the leader's: every part's top tokens
-  float marks[kWarps][kMarks];
+  __nv_bfloat16 marks[kMarks][kThreads];            // rounded up
   uint32_t groups[kGroups];                         // largest key of each group
   Stat stats[kMaxCluster];
   int befores[kMaxCluster];
@@ -337,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
 #pragma unroll
     for (int u = 1; u < kUnroll; ++u) top = max_nan(top, v[u].largest());
     best = max_nan(best, top);
-    top = warp_max_nan(top);
-    if (lane == 0) {
-      float* mark = &sh.marks[warp][round >> shift];
-      *mark = round & ((1 << shift) - 1) ? max_nan(*mark, top) : top;
+    if (top_k > 0) {
+      __nv_bfloat16* const mark = &sh.marks[round >> shift][threadIdx.x];
+      *mark = __float2bfloat16_ru(round & ((1 << shift) - 1) ? max_nan(__bfloat162float(*mark), top) : top);
     }
+    top = warp_max_nan(top);
     round_stats<T>(g, v, top, first, left, bar_ge, bar_gt);
     // (a part that fits in the queue stays there)
     if (round + kStages < rounds) fetch(first + kStages * kStep, stage);
@@ -393,32 +393,38 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
   if (top_k > 0) {
     if (static_cast<int>(threadIdx.x) < groups) raise_bar(sh, groups, top_k);
     __syncthreads();
-    // The candidates are the logits that the bar lets through, found again where a warp's mark says
-    // that there are some: of 250 stretches about as many as there are alternatives.  (Listing them
+    // The candidates are the logits that the bar lets through, found again where a thread's mark says
+    // that there are some: about as many of its stretches as there are alternatives.  (Listing them
     // while the row streams by, under a bar that rises, took more instructions than the statistics:
-    // 1024 rows of 128256 with 20 alternatives 139 us.)  Logits equal to the bar are let through
-    // unless it is a mask's value (-inf or a type's lowest), of which there are too many.
+    // 1024 rows of 128256 with 20 alternatives 139 us.  With one mark for a warp, 64 alternatives
+    // had nearly the whole row read again.)  Logits equal to the bar are let through unless it is a
+    // mask's value (-inf or a type's lowest), of which there are too many.
     const uint32_t bar_key = sh.bar;
     bool strict = !(key_value(bar_key) > -3e38f), slow = false;   // (an empty bar, 0, lets everything through)
     for (;;) {
       const float bar = bar_key == 0 ? __int_as_float(0x7fffffff) : key_value(strict ? bar_key : key_below(bar_key));
       if (end_at >= 0 && !(end <= bar)) push(sh, end, end_at);
-      for (int mark = 0; mark << shift < rounds; ++mark) {
-        if (sh.marks[warp][mark] <= bar) continue;
-        for (int round = mark << shift; round < min(rounds, (mark + 1) << shift); ++round) {
+      uint32_t look = 0;   // the stretches to look through: each lane's own, all lanes at a time
+      for (int mark = 0; mark << shift < rounds; ++mark)
+        look |= !(__bfloat162float(sh.marks[mark][threadIdx.x]) <= bar) ? 1u << mark : 0;
+      for (; look && *const_cast<volatile int*>(&sh.n_pushed) <= kPushed; look &= look - 1) {
+        const int mark = __ffs(look) - 1;
 #pragma unroll 1
-          for (int u = 0; u < kUnroll; ++u) {
-            const int at = mine0 + round * kStep + u * kThreads;
-            if (at >= v1) break;
-            Vec<T> v;
-            if (rounds <= kStages) v = queue[round * kStep + u * kThreads];
-            else v.v = body[at];
-            if (v.largest() <= bar) continue;
+        for (int round = mark << shift; round < min(rounds, (mark + 1) << shift); ++round) {
+          const int at = mine0 + round * kStep;
+          Vec<T> v[kUnroll];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (!(v[i] <= bar)) push(sh, v[i], pre + at * N + i);
-          }
-          if (*const_cast<volatile int*>(&sh.n_pushed) > kPushed) break;
+          for (int u = 0; u < kUnroll; ++u)
+            if (at + u * kThreads < v1) {
+              if (rounds <= kStages) v[u] = queue[round * kStep + u * kThreads];
+              else v[u].v = body[at + u * kThreads];
+            }
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (at + u * kThreads < v1 && !(v[u].largest() <= bar))
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                if (!(v[u][i] <= bar)) push(sh, v[u][i], pre + (at + u * kThreads) * N + i);
         }
       }
       __syncthreads();
@@ -543,13 +549,15 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
 template <class T>
 xlpk_status launch(const T* logits, long long rows, int vocab, long long stride, const int* tokens, int top_k, float* logprob,
                    float* entropy, int* rank, int* top_ids, float* top_logprobs, int sms, cudaStream_t st) {
+  // Parts keep the GPU busy while a thread still has two vectors or more: a row of 32000 takes 6.7 us
+  // whole and 4.4 in 8 parts (fp32, no alternatives), 64 rows of 128256 20.5 whole, 11.8 in 4, 14.9 in
+  // 8 (they no longer fit at once), 1024 rows 92.6 whole and 108 in 4.
   int parts = 1;
   while (parts < kMaxCluster && rows * parts * 2 <= 3 * sms && vocab / (parts * 2) >= 2 * kThreads * Vec<T>::N) parts *= 2;
   static std::atomic<unsigned long long> ready;   // devices whose kernel has its attributes
   int dev = 0;
   XLPK_CUDA(cudaGetDevice(&dev));
   if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    XLPK_CUDA(cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     XLPK_CUDA(cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared) + kQueueBytes));
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
