@@ -97,6 +97,24 @@ struct Vec {
     if (sizeof(T) == 4) return __uint_as_float(w[i]);
     return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+  // How many are not <= `bar` (a value of T), or, with `equal`, not < it.
+  __device__ int before(float bar, bool equal) const {
+    int n = 0;
+    if (sizeof(T) == 4) {
+      const float b = !equal ? bar : bar == -INFINITY ? __int_as_float(0x7fffffff) : key_value(key_below(order_key(bar)));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        asm("{ .reg .pred p; setp.gtu.f32 p, %1, %2; @p add.s32 %0, %0, 1; }" : "+r"(n) : "f"((*this)[i]), "f"(b));
+      return n;
+    }
+    // two at a time, as 1 and 0, which bf16 adds exactly
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+    const __nv_bfloat162 b = __float2bfloat162_rn(bar);
+    __nv_bfloat162 sum = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __hadd2(sum, equal ? __hgeu2(p[i], b) : __hgtu2(p[i], b));
+    return static_cast<int>(__low2float(sum) + __high2float(sum));
+  }
   // NaN if there is one
   __device__ float largest() const {
     if (sizeof(T) == 4) return max_nan(max_nan((*this)[0], (*this)[1]), max_nan((*this)[2], (*this)[3]));
@@ -166,59 +184,47 @@ static_assert(kPushed <= kMaxCluster * kMaxTop, "candidates");
 
 // Statistics and rank of one round: the thread's vectors, those past the part's end all -inf,
 // which adds nothing to either (`left`: the vectors wholly to the left of the token that the part
-// has); `top` the warp's largest logit, or NaN.
+// has; `mine`: the token's logit); `top` the warp's largest logit, or NaN.
 template <class T>
-__device__ inline void round_stats(Gather& g, const Vec<T> (&v)[kUnroll], float top, int first, int left, float bar_ge,
-                                   float bar_gt) {
+__device__ inline void round_stats(Gather& g, const Vec<T> (&v)[kUnroll], float top, int first, int left, float mine) {
   constexpr int N = Vec<T>::N;
+  if (!(top < mine)) {   // (few rounds have larger ones if it is a likely token)
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) g.before += v[u].before(mine, first + u * kThreads < left);
+  }
+  float x[kUnroll * N];
+#pragma unroll
+  for (int i = 0; i < kUnroll * N; ++i) x[i] = v[i / N][i % N];
   if (top >= g.m) {
-    // the maximum stands here: its ties are counted, not added
     if (top > g.m) g.rise(top);
-    if (top > -INFINITY) {
+    if (top == -INFINITY) return;
+    // the maximum stands here: it is counted, and what is added in its place is 0
+    const float far = top - fmaxf(700.f, fabsf(top));   // (NaN for +inf)
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < N; ++i) g.any(v[u][i]);
-    }
-  } else {
-    float s = 0.f, t = 0.f;
-    if (!g.careful) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float y = fmaf(v[u][i], kLog2e, -g.base), e = ex2(y);
-          s += e;
-          t = fmaf(e, y, t);
-        }
-      g.careful = t != t;
-    }
-    if (g.careful) {
-      s = t = 0.f;
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float y = max_nan(fmaf(v[u][i], kLog2e, -g.base), -1000.f), e = ex2(y);
-          s += e;
-          t = fmaf(e, y, t);
-        }
-    }
-    g.s += s;
-    g.t += t;
+    for (int i = 0; i < kUnroll * N; ++i)
+      if (x[i] == top) x[i] = far, ++g.ties;
   }
-  if (!(top < bar_gt)) {   // (bar_gt is the token's logit: few rounds have larger ones if it is a likely token)
+  float s = 0.f, t = 0.f;
+  if (!g.careful) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const float bar = first + u * kThreads < left ? bar_ge : bar_gt;
+    for (int i = 0; i < kUnroll * N; ++i) {
+      const float y = fmaf(x[i], kLog2e, -g.base), e = ex2(y);
+      s += e;
+      t = fmaf(e, y, t);
+    }
+    g.careful = t != t;
+  }
+  if (g.careful) {
+    s = t = 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        uint32_t larger;
-        asm("set.gtu.u32.f32 %0, %1, %2;" : "=r"(larger) : "f"(v[u][i]), "f"(bar));
-        g.before -= static_cast<int>(larger);
-      }
+    for (int i = 0; i < kUnroll * N; ++i) {
+      const float y = max_nan(fmaf(x[i], kLog2e, -g.base), -1000.f), e = ex2(y);
+      s += e;
+      t = fmaf(e, y, t);
     }
   }
+  g.s += s;
+  g.t += t;
 }
 
 // Raises the bar to the (top_k + 1)-th largest of the groups' keys: at least so many logits
@@ -292,11 +298,10 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
   if (threadIdx.x == 0) sh.n_pushed = 0, sh.bar = 0;
   __syncthreads();
 
-  // A logit comes before the token's if it is not <= gt, or, to the left of the token, not <= ge: the
-  // float below the token's (NaN, and so everything, if there is none).  tok_vec: the vectors wholly to the left.
+  // A logit comes before the token's if it is not <= it, or, to the left of the token, not < it.
+  // tok_vec: the vectors wholly to the left.
   const int tok_vec = tok < pre ? 0 : (tok - pre) / N, left = min(tok_vec, v1);
   const uint32_t my_key = order_key(mine);
-  const float bar_gt = mine, bar_ge = mine == -INFINITY ? __int_as_float(0x7fffffff) : key_value(key_below(my_key));
 
   // the ends, one logit of a thread at most
   Gather g;
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
     if (top > -INFINITY) g.rise(top);
     if (end_at >= 0) {
       if (top > -INFINITY) g.any(end);
-      g.before = !(end <= (end_at < tok ? bar_ge : bar_gt));
+      g.before = !(end <= mine) || (end_at < tok && !(end < mine));
       best = end;
     }
     if (top != top) g.t = top;
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
       *mark = __float2bfloat16_ru(round & ((1 << shift) - 1) ? max_nan(__bfloat162float(*mark), top) : top);
     }
     top = warp_max_nan(top);
-    round_stats<T>(g, v, top, first, left, bar_ge, bar_gt);
+    round_stats<T>(g, v, top, first, left, mine);
     // (a part that fits in the queue stays there)
     if (round + kStages < rounds) fetch(first + kStages * kStep, stage);
     else asm volatile("cp.async.commit_group;" ::: "memory");
