@@ -97,9 +97,11 @@ struct Shape {
   static constexpr bool KV8 = KV8_;      // e4m3 cache, fp16 operands; else bf16
   static constexpr bool WIDE = WIDE_;    // 9 to 16 query heads per kv head; else up to 8
   static constexpr bool IO32 = IO32_;
-  // e4m3 tiles are half the bytes for the same work: more warps, as far as registers and queue go
-  // (four sequences of 131072, d 128: 8 warps 255 us, 12 245, 16 411; 16 of 8192, d 64: 57, 53, 49)
-  static constexpr int WARPS = WIDE || !KV8 ? 8 : D == 128 ? 12 : 16, THREADS = WARPS * 32;
+  // Eight warps have registers for four chains of MMAs.  e4m3 rows of 64 leave enough for twelve and
+  // two chains (16 sequences of 8192, d 64: 8 warps 53 us, 12 46, 16 48; four of 131072, d 128: 8 warps
+  // 233 us, 12, which spill, 246).
+  static constexpr int WARPS = !WIDE && KV8 && D == 64 ? 12 : 8, THREADS = WARPS * 32;
+  static constexpr int CHAINS = WARPS == 8 ? 4 : 2;   // scores' chains of MMAs that run at once
   static constexpr int E = KV8 ? 1 : 2;
   static constexpr int ROWS = WIDE ? 16 : 8;
   // what one lane copies of a cache row: a K row is read by the 4 lanes of a quad in 16-byte
@@ -123,11 +125,11 @@ struct Shape {
 __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
                            bool f16) {
   if (f16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -548,48 +550,52 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
       asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
       __syncwarp();   // V was copied by other lanes too
       const int stage2 = stage + 1 == S::STAGES ? 0 : stage + 1;
-      // ---- scores: positions are the columns, two tiles side by side
+      // ---- scores: positions are the columns, two tiles side by side, so that four chains of MMAs
+      // run at once.  (Where there is no second tile, what is in its slot is multiplied and masked.)
       float s[4][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint8_t* at = queue_at + (half ? stage2 : stage) * S::STAGE;
+      for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2) {
-          float(&sc)[4] = s[half * 2 + n2];
-          sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
-          if (half && !pair) continue;
+      for (int n0 = 0; n0 < 4; n0 += S::CHAINS)
 #pragma unroll
-          for (int j = 0; j < S::KC; ++j) {
-            const uint4 k4 = *reinterpret_cast<const uint4*>(at + ((n2 * S::KC + j) * 32 + lane) * 16);
-            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
-            uint32_t kb[8];
-            constexpr int NB = S::KV8 ? 8 : 4;
+      for (int j = 0; j < S::KC; ++j) {
+        constexpr int NB = S::KV8 ? 8 : 4;
+        uint32_t kb[S::CHAINS][NB];
 #pragma unroll
-            for (int i2 = 0; i2 < 4; ++i2) {
-              if (S::KV8)
-                kb[2 * i2] = widen(kw[i2]), kb[2 * i2 + 1] = widen_high(kw[i2]);
-              else
-                kb[i2] = kw[i2];
-            }
+        for (int i = 0; i < S::CHAINS; ++i) {
+          const int nt = n0 + i;
+          const uint4 k4 = *reinterpret_cast<const uint4*>(queue_at + (nt >> 1 ? stage2 : stage) * S::STAGE +
+                                                           (((nt & 1) * S::KC + j) * 32 + lane) * 16);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-            for (int p = 0; p < NB; p += 2) {
-              const int c = j * NB + p;
-              if (S::WIDE) {
-#pragma unroll
-                for (int k = 0; k < S::QT; ++k)
-                  mma(sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[p], kb[p + 1], S::KV8);
-              } else {
-                if (S::QT > 1)
-                  mma(sc, q[0][0][c], q[0][S::QT > 1][c], q[0][0][c + 1], q[0][S::QT > 1][c + 1], kb[p], kb[p + 1], S::KV8);
-                else
-                  mma(sc, q[0][0][c], 0, q[0][0][c + 1], 0, kb[p], kb[p + 1], S::KV8);
-                if (S::QT > 2) mma(sc, q[0][S::QT - 1][c], 0, q[0][S::QT - 1][c + 1], 0, kb[p], kb[p + 1], S::KV8);
-              }
-            }
+          for (int i2 = 0; i2 < 4; ++i2) {
+            if (S::KV8)
+              kb[i][(2 * i2) % NB] = widen(kw[i2]), kb[i][(2 * i2 + 1) % NB] = widen_high(kw[i2]);
+            else
+              kb[i][i2] = kw[i2];
           }
-          if (!S::WIDE && S::QT > 1) sc[0] += sc[2], sc[1] += sc[3];
+        }
+#pragma unroll
+        for (int p = 0; p < NB; p += 2) {
+          const int c = j * NB + p;
+#pragma unroll
+          for (int k = 0; k < (S::WIDE ? S::QT : (S::QT + 1) / 2); ++k)
+#pragma unroll
+            for (int i = 0; i < S::CHAINS; ++i) {
+              float(&sc)[4] = s[n0 + i];
+              if (S::WIDE)
+                mma(sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[i][p], kb[i][p + 1], S::KV8);
+              else if (2 * k + 1 < S::QT)
+                mma(sc, q[0][2 * k][c], q[0][(2 * k + 1) % S::QT][c], q[0][2 * k][c + 1], q[0][(2 * k + 1) % S::QT][c + 1],
+                    kb[i][p], kb[i][p + 1], S::KV8);
+              else
+                mma(sc, q[0][2 * k][c], 0, q[0][2 * k][c + 1], 0, kb[i][p], kb[i][p + 1], S::KV8);
+            }
         }
       }
+      if (!S::WIDE && S::QT > 1)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
       // ---- online softmax over the two tiles
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -925,15 +931,15 @@ xlpk_status launch_for(const Args& args, int ctas, cudaStream_t st) {
   return io32 ? launch<Shape<D, KV8, false, true>>(args, ctas, st) : launch<Shape<D, KV8, false, false>>(args, ctas, st);
 }
 
-constexpr int kMaxWorkers = kMaxCtas * 16;
+constexpr int kMaxWorkers = kMaxCtas * 12;
 constexpr int64_t kJoinBytes = (kMaxWorkers + 1) * sizeof(int4);
 
 }  // namespace
 
 extern "C" int64_t xlpk_decode_attention_workspace(const xlpk_attention_args* a) {
   if (!shape_ok(a)) return 0;
-  // (16 warps of 8 rows, or 8 of 16)
-  return kJoinBytes + kMaxWorkers * 2 * 8 * (static_cast<int64_t>(a->head_dim) + 2) * 4;
+  // (12 warps of 8 rows at most, or 8 of 16)
+  return kJoinBytes + kMaxCtas * 8 * 2 * 16 * (static_cast<int64_t>(a->head_dim) + 2) * 4;
 }
 
 extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void* workspace_dev, int64_t workspace_bytes,
