@@ -118,6 +118,7 @@ struct Shape {
   static constexpr int QT = IO32 ? (KV8 ? 2 : 3) : 1;   // terms of q
   static constexpr int PT = IO32 && !KV8 ? 3 : 2;       // terms of p
   static constexpr int QR = D / 8;                      // registers of one term of one row
+  static constexpr bool LOW = WIDE && QT > 1;           // the lower terms' scores have sums of their own (else: rows 8-15)
   static constexpr int SHIFT = KV8 ? 10 : 0;            // p is held times 2^SHIFT
   static constexpr int SLOT = ROWS * (D + 2);           // floats of a partial result
 };
@@ -555,6 +556,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
       float s[4][4];
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      float low[S::LOW ? 4 : 1][4] = {};   // what the lower terms add: each sum loses its own last bits only
 #pragma unroll
       for (int n0 = 0; n0 < 4; n0 += S::CHAINS)
 #pragma unroll
@@ -584,18 +586,25 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
             for (int i = 0; i < S::CHAINS; ++i) {
               float(&sc)[4] = s[n0 + i];
               if (S::WIDE)
-                mma(sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[i][p], kb[i][p + 1], S::KV8);
+                mma(S::LOW && k > 0 ? low[(n0 + i) * S::LOW] : sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[i][p], kb[i][p + 1], S::KV8);
               else if (2 * k + 1 < S::QT)
                 mma(sc, q[0][2 * k][c], q[0][(2 * k + 1) % S::QT][c], q[0][2 * k][c + 1], q[0][(2 * k + 1) % S::QT][c + 1],
                     kb[i][p], kb[i][p + 1], S::KV8);
               else
-                mma(sc, q[0][2 * k][c], 0, q[0][2 * k][c + 1], 0, kb[i][p], kb[i][p + 1], S::KV8);
+                // (a third term joins the second)
+                mma(sc, S::QT > 1 ? 0 : q[0][2 * k][c], S::QT > 1 ? q[0][2 * k][c] : 0, S::QT > 1 ? 0 : q[0][2 * k][c + 1],
+                    S::QT > 1 ? q[0][2 * k][c + 1] : 0, kb[i][p], kb[i][p + 1], S::KV8);
             }
         }
       }
       if (!S::WIDE && S::QT > 1)
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
+      if (S::LOW)
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[nt][c] += low[nt * S::LOW][c];
       // ---- online softmax over the two tiles
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -653,7 +662,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
             for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][lo], pt[NR - 1][k][lo], pt[0][k][hi], pt[NR - 1][k][hi], b0, b1, S::KV8);
           } else {
             mma(c, pt[0][0][lo], pt[0][1][lo], pt[0][0][hi], pt[0][1][hi], b0, b1, S::KV8);
-            if (S::PT > 2) mma(c, pt[0][S::PT - 1][lo], 0, pt[0][S::PT - 1][hi], 0, b0, b1, S::KV8);
+            if (S::PT > 2) mma(c, 0, pt[0][S::PT - 1][lo], 0, pt[0][S::PT - 1][hi], b0, b1, S::KV8);
           }
         };
         const int slot = half ? stage2 : stage;
