@@ -879,15 +879,15 @@ xlpk_status check_args(const xlpk_attention_args* a) {
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: io_dtype is bf16 or fp32, kv_dtype bf16 or e4m3");
   if (a->n_pages < 0 || a->page_size < 1 || a->table_cols < 0 || a->window < 0 || a->sinks < 0)
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: a negative count");
-  if (static_cast<int64_t>(a->table_cols) * a->page_size > INT32_MAX)
-    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: a table of 2^31 positions or more");
+  if (static_cast<int64_t>(a->table_cols) * a->page_size > INT32_MAX - 4 * kTile)
+    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: a capacity of 2^31 - 64 positions or more");
   if (!(a->scale > 0) || !std::isfinite(a->scale))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: scale is not finite and positive");
   if (a->kv_dtype == XLPK_DTYPE_FP8_E4M3 && (!power_of_two_scale(a->k_scale) || !power_of_two_scale(a->v_scale)))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: cache scales are powers of two in [2^-24, 2^24]");
   if (static_cast<int64_t>(a->n_seqs) * a->n_kv_heads >
       INT32_MAX / (static_cast<int64_t>(a->table_cols) * a->page_size / kTile + 2))
-    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: n_seqs * n_kv_heads * capacity of 16 * 2^31 or more");
+    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: n_seqs * n_kv_heads * capacity of about 2^35 positions or more");
   if (a->n_seqs == 0) return XLPK_OK;
   if (!a->q_dev || !a->seq_lens_dev || !a->out_dev || (!a->k_new_dev) != (!a->v_new_dev) ||
       ((!a->k_dev || !a->v_dev) && a->n_pages > 0))
@@ -902,9 +902,10 @@ xlpk_status check_args(const xlpk_attention_args* a) {
   bool ok = aligned(a->q_dev, 16) && aligned(a->out_dev, 16) && aligned(a->k_new_dev, 16) && aligned(a->v_new_dev, 16) &&
             aligned(a->k_dev, 16) && aligned(a->v_dev, 16) && aligned(a->page_table_dev, 4) &&
             aligned(a->seq_lens_dev, 4) && aligned(a->lse_dev, 4) && aligned(a->status_dev, 4);
-  for (int64_t s : io_strides) ok = ok && (s * io) % 16 == 0;
-  for (int64_t s : kv_strides) ok = ok && (s * kv) % 16 == 0;
-  if (!ok) return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: a pointer or stride is not a multiple of 16 bytes");
+  for (int64_t s : io_strides) ok = ok && s >= 0 && (s * io) % 16 == 0;
+  for (int64_t s : kv_strides) ok = ok && s >= 0 && (s * kv) % 16 == 0;
+  ok = ok && a->table_stride >= 0;
+  if (!ok) return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: a pointer or stride is not a multiple of 16 bytes, or negative");
   return XLPK_OK;
 }
 

@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
   const int part = blockIdx.x - static_cast<int>(r) * parts;
   const T* x = logits + r * stride;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");   // this CTA runs: its memory may be written
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed;");   // this CTA runs: its memory may be written
   // whole vectors of the row are [pre, pre + N * vecs); what is left at its ends goes to the first and last part
   const int pre = min(vocab, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
   const int vecs = (vocab - pre) / N, v0 = static_cast<int>(static_cast<long long>(vecs) * part / parts),
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
 
   // ---- the parts joined by the first of them
   if (parts > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
     if (part != 0) {
       uint32_t leader;
       const uint32_t here = static_cast<uint32_t>(__cvta_generic_to_shared(&sh));
@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprobs_kernel(const T* logits, 
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at(&sh.befores[part])), "r"(before) : "memory");
       }
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (part != 0) return;
   }
   if (warp == kWarps - 1) {
@@ -593,6 +593,7 @@ extern "C" xlpk_status xlpk_token_logprobs(const void* logits_dev, int32_t dtype
   if (rows < 0 || vocab < 1 || row_stride < 0 || top_k < 0 || top_k > vocab)
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_token_logprobs: rows, vocab, row_stride or top_k");
   if (top_k > kMaxTop) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_token_logprobs: top_k over 64");
+  if (vocab > 1 << 30) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_token_logprobs: a vocabulary over 2^30");
   if (rows > INT32_MAX) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_token_logprobs: 2^31 rows or more");
   int sms = 0;
   if (rows > 0) {

@@ -203,12 +203,13 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const xlpk_pag
     return;
   }
   const long long head = static_cast<long long>(p.page_size) * p.row_bytes, page = head * p.n_kv_heads;
-  const int segs = static_cast<int>((head + kSegment - 1) / kSegment), per_copy = p.n_layers * 2 * p.n_kv_heads * segs;
-  for (long long u = blockIdx.x - table_blocks; u < static_cast<long long>(copies) * per_copy; u += gridDim.x - table_blocks) {
-    const int k = static_cast<int>(u / per_copy), w = static_cast<int>(u % per_copy), seg = w % segs, h = w / segs % p.n_kv_heads,
-              plane = w / segs / p.n_kv_heads;   // K and V of each layer
-    uint8_t* pool = static_cast<uint8_t*>(plane & 1 ? p.v_dev : p.k_dev) + static_cast<long long>(plane >> 1) * p.n_pages * page + h * head;
-    copy_segment(pool + f.dst[k] * page, pool + f.src[k] * page, static_cast<long long>(seg) * kSegment,
+  const long long segs = (head + kSegment - 1) / kSegment, per_copy = p.n_layers * 2ll * p.n_kv_heads * segs;
+  for (long long u = blockIdx.x - table_blocks; u < copies * per_copy; u += gridDim.x - table_blocks) {
+    const int k = static_cast<int>(u / per_copy);
+    const long long w = u - k * per_copy, run = w / segs, plane = run / p.n_kv_heads;   // K and V of each layer
+    uint8_t* pool = static_cast<uint8_t*>(plane & 1 ? p.v_dev : p.k_dev) + (plane >> 1) * p.n_pages * page +
+                    (run - plane * p.n_kv_heads) * head;
+    copy_segment(pool + f.dst[k] * page, pool + f.src[k] * page, (w - run * segs) * kSegment,
                  static_cast<long long>(f.filled[k]) * p.row_bytes);
   }
 }

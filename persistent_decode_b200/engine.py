@@ -241,6 +241,9 @@ class Engine:
         SCORE_BYTES (or one step), whatever n."""
         import torch
         from .ops import TokenLogprobs, token_logprobs
+        cache = self._refs[1]
+        if tokens.dim() != 2 or tokens.shape[1] != self.B or tokens.dtype != torch.int32 or tokens.device != cache.device:
+            raise ValueError(f"tokens must be int32 [n][{self.B}] on {cache.device}")
         n = int(tokens.shape[0])
         tokens = tokens.contiguous()
         dev, V = tokens.device, self.cfg.vocab

@@ -194,17 +194,20 @@ def decode_attention(q, k_cache, v_cache, seq_lens, page_table=None, *, k_new=No
             out = _empty((B, H, D), q.dtype)
         lse = _empty((B, H), torch.float32) if return_lse else None
         os = out.stride()
-        args = _ATTENTION.pack(
-            q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), table_at, seq_lens.data_ptr(), out.data_ptr(),
-            _ptr(lse), _ptr(status),
-            0 if one_b else qs[0], 0 if one_h else qs[1],
-            0 if one_b else nk0, 0 if one_kh else nk1, 0 if one_b else nv0, 0 if one_kh else nv1,
-            0 if one_b else os[0], 0 if one_h else os[1],
-            0 if one_p else ks[0], 0 if one_kh else ks[1], 0 if one_pos else ks[2],
-            0 if one_p else vs[0], 0 if one_kh else vs[1], 0 if one_pos else vs[2], table_step,
-            B, H, KH, D, n_pages, P, cols, _IO[q.dtype], _KV[k_cache.dtype],
-            _int32(window, "window"), _int32(sinks, "sinks"),
-            D ** -0.5 if scale is None else scale, k_scale, v_scale)
+        try:
+            args = _ATTENTION.pack(
+                q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), table_at, seq_lens.data_ptr(), out.data_ptr(),
+                _ptr(lse), _ptr(status),
+                0 if one_b else qs[0], 0 if one_h else qs[1],
+                0 if one_b else nk0, 0 if one_kh else nk1, 0 if one_b else nv0, 0 if one_kh else nv1,
+                0 if one_b else os[0], 0 if one_h else os[1],
+                0 if one_p else ks[0], 0 if one_kh else ks[1], 0 if one_pos else ks[2],
+                0 if one_p else vs[0], 0 if one_kh else vs[1], 0 if one_pos else vs[2], table_step,
+                B, H, KH, D, n_pages, P, cols, _IO[q.dtype], _KV[k_cache.dtype],
+                _int32(window, "window"), _int32(sinks, "sinks"),
+                D ** -0.5 if scale is None else scale, k_scale, v_scale)
+        except (struct.error, OverflowError, TypeError) as e:
+            raise ValueError(f"scale, k_scale or v_scale: {e}") from None
         key = (KH > 0 and H > 8 * KH, D)
         need = _WORKSPACE.get(key)
         if need is None:

@@ -149,6 +149,24 @@ def test_split_and_joined(cuda_device, B, n):
     check(s, *call(s))
 
 
+@pytest.mark.parametrize("H,KH,D,kv,io", [(16, 1, 128, "bf16", torch.bfloat16), (16, 1, 128, "e4m3", torch.float32),
+                                          (12, 1, 64, "bf16", torch.float32), (8, 2, 64, "e4m3", torch.bfloat16),
+                                          (7, 1, 128, "bf16", torch.float32), (10, 2, 64, "e4m3", torch.float32)])
+@pytest.mark.parametrize("B,most", [(300, 90), (170, 700), (2, 6000)])
+def test_many_short_and_few_long_sequences(cuda_device, B, most, H, KH, D, kv, io):
+    # segments that warps share, that CTAs share, and that are cut into pieces either way
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, most + 1, (B,), generator=g).tolist()
+    lens[0] = most
+    s = make(B, lens, H, KH, D, 48, kv, io, seed=B + H)
+    check(s, *call(s))
+
+
+def test_one_sequence_outlasts_all_others(cuda_device):
+    s = make(400, [9000] + [3] * 399, 4, 2, 64, 16, seed=2)
+    check(s, *call(s))
+
+
 def test_ragged_lengths_share_the_work(cuda_device):
     lens = [5, 9000, 0, 1, 333, 0, 2500, 16]
     s = make(len(lens), lens, 8, 2, 128, 64, "e4m3", torch.float32, seed=3)
@@ -297,12 +315,15 @@ def test_refusals(cuda_device):
                                          k_new=q[:, :2], v_new=q[:, :2]),
                 lambda: decode_attention(q.cpu(), k, v, lens, table),
                 lambda: decode_attention(q, k, v, lens.cpu(), table),
-                lambda: decode_attention(q.transpose(1, 2), k, v, lens, table)):
+                lambda: decode_attention(q.transpose(1, 2), k, v, lens, table),
+                lambda: decode_attention(q, k, v, lens, table, window=1 << 40),
+                lambda: decode_attention(q, k, v, lens, table, k_new=q[:, :2])):
         with pytest.raises(ValueError):
             bad()
     odd = torch.zeros(2 * 4 * 64 + 1, dtype=torch.bfloat16, device=cuda_device)[1:].view(2, 4, 64)
     for bad in (lambda: decode_attention(odd, k, v, lens, table), lambda: decode_attention(q, k, v, lens, table, window=-1),
-                lambda: decode_attention(q, k, v, lens, table, scale=float("nan"))):
+                lambda: decode_attention(q, k, v, lens, table, scale=float("nan")),
+                lambda: decode_attention(q, k, v, lens, table, scale=1e60)):
         with pytest.raises(XlpkError) as e:
             bad()
         assert e.value.status == _abi.XLPK_ERR_INVALID_ARG

@@ -115,6 +115,27 @@ def test_masks_ties_and_infinities(cuda_device, V, dtype):
             check(x, tok, run(x, tok, k), k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_large_logits_of_one_thread(cuda_device, dtype):
+    # every large logit falls to the vectors that one thread of a part reads, so that what the other
+    # threads have bounds the alternatives far below them, and more pass that bound than are ranked
+    V, g = 700001, torch.Generator().manual_seed(11)
+    x = torch.randn(2, V, generator=g)
+    n = 16 // dtype.itemsize
+    vec = torch.arange(V) // n
+    x[:, vec % 256 == 5] += 60
+    x = x.to(dtype)
+    for k in (5, 64):
+        check(x, [7, V - 1], run(x, [7, V - 1], k), k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_nan_nearly_everywhere(cuda_device, dtype):
+    x = torch.full((2, 9001), math.nan, dtype=dtype)
+    x[:, 100:103] = torch.tensor([1.0, 2.0, 3.0]).to(dtype)
+    check(x, [101, 8999], run(x, [101, 8999], 64), 64)
+
+
 def test_a_certain_token_keeps_its_small_logprob(cuda_device):
     # log p of the best token is -s with s = 9 e^-20: far below the step of 1, kept to relative 2^-13
     x = torch.zeros(1, 10)

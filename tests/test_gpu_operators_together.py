@@ -76,6 +76,11 @@ def test_score_matches_the_oracle(cuda_device):
         inp = toks[s].tolist()
     empty = m.engine.score(toks[:0].to(cuda_device))
     assert empty.logprob.shape == (0, 2)
+    for bad in (toks.long().to(cuda_device), toks, toks[:, :1].to(cuda_device), toks[0].to(cuda_device)):
+        with pytest.raises(ValueError):
+            m.engine.score(bad)
+    with pytest.raises(ValueError):     # a contiguous cache has no pages
+        m.engine.page_pool(torch.zeros(2, dtype=torch.int32, device=cuda_device))
 
 
 def test_score_in_parts_is_the_same(cuda_device, monkeypatch):

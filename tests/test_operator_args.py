@@ -41,7 +41,8 @@ def _attn(**kw):
     dict(kv_dtype=_abi.XLPK_DTYPE_FP8_E4M3, k_scale=0.3), dict(kv_dtype=_abi.XLPK_DTYPE_FP8_E4M3, v_scale=2.0 ** 25),
     dict(q_dev=0), dict(q_dev=P + 8), dict(out_dev=P + 4), dict(k_dev=0), dict(v_dev=P + 2), dict(seq_lens_dev=0),
     dict(seq_lens_dev=P + 2), dict(k_new_dev=P), dict(v_new_dev=P), dict(k_pos_stride=65), dict(v_head_stride=4),
-    dict(q_head_stride=66), dict(out_seq_stride=1), dict(page_table_dev=0), dict(page_table_dev=0, table_cols=1)],
+    dict(q_head_stride=66), dict(out_seq_stride=1), dict(k_page_stride=-2 * 16 * 64), dict(q_seq_stride=-256),
+    dict(table_stride=-8), dict(page_table_dev=0), dict(page_table_dev=0, table_cols=1)],
     ids=lambda d: ",".join(f"{k}={v}" for k, v in d.items()))
 def test_attention_refuses_invalid(lib, bad):
     a = _attn(**bad)
@@ -50,7 +51,9 @@ def test_attention_refuses_invalid(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(head_dim=96), dict(head_dim=256), dict(n_q_heads=34, n_kv_heads=2),
-                                 dict(table_cols=1 << 20, page_size=1 << 12)])
+                                 dict(table_cols=1 << 20, page_size=1 << 12),
+                                 dict(table_cols=1, page_size=(1 << 31) - 1),
+                                 dict(n_seqs=1 << 20, n_q_heads=64, n_kv_heads=64, table_cols=1 << 16)])
 def test_attention_refuses_unsupported(lib, bad):
     a = _attn(**bad)
     assert lib.xlpk_decode_attention(C.byref(a), P, 1 << 30, None) == UNSUPPORTED
@@ -138,6 +141,7 @@ def test_logprobs_refuse_bad_arguments(lib):
         assert lib.xlpk_last_cuda_error().startswith(b"xlpk_token_logprobs:"), bad
     assert call(k=65) == UNSUPPORTED
     assert call(rows=1 << 31) == UNSUPPORTED
+    assert call(vocab=(1 << 30) + 1, stride=(1 << 30) + 1) == UNSUPPORTED
 
 
 def test_struct_layout_matches_header(tmp_path):
