@@ -290,6 +290,24 @@ def test_on_another_stream(cuda_device):
     assert torch.equal(got, want) and torch.equal(other, want)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(cuda_device, kv):
+    # the same few pages at both ends of pools of more than 2^32 bytes
+    small = make(2, [300, 77], 4, 1, 128, 64, kv, seed=17)
+    want, _ = call(small)
+    pages = (1 << 32) // (64 * 128 * small["k"].element_size()) + 1000
+    n = small["k"].shape[0]
+    where = torch.arange(n, device=cuda_device) + torch.where(torch.arange(n, device=cuda_device) % 2 == 0, pages - n, 0)
+    big = dict(small)
+    for name in ("k", "v"):
+        big[name] = torch.empty((pages, *small[name].shape[1:]), dtype=small[name].dtype, device=cuda_device)
+        big[name][where] = small[name]
+    t = small["table"]
+    big["table"] = torch.where((t >= 0) & (t < n), where[t.clamp(0, n - 1).long()].int(), t)
+    got, _ = call(big)
+    assert torch.equal(got, want)
+
+
 def test_no_sequences(cuda_device):
     s = make(1, [5], 4, 2, 64, 16)
     got = decode_attention(s["q"][:0], s["k"], s["v"], s["lens"][:0], s["table"][:0])

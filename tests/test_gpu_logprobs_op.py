@@ -205,6 +205,15 @@ def test_same_bits_every_time_and_in_graphs(cuda_device):
     assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
 
 
+def test_offsets_past_32_bits(cuda_device):
+    flat = torch.empty((1 << 32) + 5000, dtype=torch.bfloat16, device=cuda_device)
+    x = flat.as_strided((3, 4099), (1 << 31, 1))
+    host = (torch.randn(3, 4099, generator=torch.Generator().manual_seed(3)) * 2).to(torch.bfloat16)
+    x.copy_(host)
+    r = token_logprobs(x, torch.tensor([0, 4098, 17], dtype=torch.int32, device=cuda_device), top_k=7)
+    check(host, [0, 4098, 17], type(r)(*(f.cpu() for f in r)), 7)
+
+
 def test_refusals(cuda_device):
     x = torch.zeros(4, 100, device=cuda_device)
     tok = torch.zeros(4, dtype=torch.int32, device=cuda_device)

@@ -337,6 +337,31 @@ def test_on_another_stream(cuda_device):
     same(h, p)
 
 
+def test_offsets_past_32_bits(cuda_device):
+    # one layer of K and V of more than 2^32 bytes each; pages at its end are copied, forked and moved to its start
+    P, n = 1024, (1 << 32) // (1024 * 128) + 64
+    k, v = (torch.empty((1, n, 1, P, 128), dtype=torch.uint8, device=cuda_device) for _ in range(2))
+    refs = torch.zeros(n, dtype=torch.int32, device=cuda_device)
+    refs[n - 2:] = 1
+    g = torch.Generator(device=cuda_device).manual_seed(1)
+    for t in (k, v):
+        t[:, n - 2:] = torch.randint(0, 256, t[:, n - 2:].shape, dtype=torch.uint8, generator=g, device=cuda_device)
+    full, part = [t[0, n - 2].clone() for t in (k, v)], [t[0, n - 1].clone() for t in (k, v)]
+    table, lens = i32([[n - 2, n - 1, -1], [-1, -1, -1]]), i32([P + 700, 0])
+    p = PagePool(k, v, table, lens, refs)
+    p.copy([n - 2], [n - 3])
+    p.fork(i32([0, 0]))
+    p.check()
+    assert table.tolist() == [[n - 2, n - 1, -1], [n - 2, 0, -1]]
+    for t, f, q in zip((k, v), full, part):
+        assert torch.equal(t[0, n - 3], f) and torch.equal(t[0, 0, :, :700], q[:, :700])
+    remap = p.compact()
+    p.check()
+    assert table.tolist() == [[1, 2, -1], [1, 0, -1]] and remap[n - 2:].tolist() == [1, 2]
+    for t, f, q in zip((k, v), full, part):
+        assert torch.equal(t[0, 1], f) and torch.equal(t[0, 2], q)
+
+
 def test_refusals(cuda_device):
     h, p = make(2, 4, 8, 12, [20, 9])
     k, v, t, n, r = p.k, p.v, p.page_table, p.seq_lens, p.refs
