@@ -458,6 +458,8 @@ xlpk_status xlpk_tc_gemm_tile(const void* w_dev, int32_t n, int32_t k, const flo
  *    status_dev: of 4).
  *  - n = 0: the output row is zero, lse -inf, nothing is stored.
  *  - q and the visible entries are finite; what stands elsewhere may be anything.
+ *  - Capacities (table_cols * page_size) below 2^31 - 64 positions, and below about
+ *    2^35 over all sequences and kv heads (else XLPK_ERR_UNSUPPORTED).
  *  - Rows of the cache that no sequence sees are not read: pages a window has
  *    passed may be gone from the table.  A visible position whose page lies
  *    outside [0, n_pages), or a length outside [0, table_cols * page_size], makes
@@ -500,9 +502,9 @@ xlpk_status xlpk_decode_attention(const xlpk_attention_args* args, void* workspa
 /* The pages of a paged cache and who holds them.  The pools are those of
  * xlpk_kv with any page size: K and V each [n_layers][n_pages][n_kv_heads]
  * [page_size][row_bytes].  Row r of the table is a sequence of seq_lens[r]
- * positions; an entry of -1 holds no page.  refs[p] counts the entries that
- * name page p, plus the references that the caller keeps besides (a prefix held
- * for later); a page with refs 0 is free.  Table, lengths and counts are device
+ * positions; an entry outside [0, n_pages) holds no page (the calls write -1).
+ * refs[p] counts the entries that name page p, plus the references that the
+ * caller keeps besides (a prefix held for later); a page with refs 0 is free.  Table, lengths and counts are device
  * memory that the calls update in place, so a loop of them with decode calls
  * needs no host copy.  Fresh pages are always the lowest-numbered free ones, in
  * row order: results do not depend on timing.
@@ -564,8 +566,9 @@ xlpk_status xlpk_pages_copy(const xlpk_page_pool* pool, const int32_t* src_host,
  *     top_ids / top_logprobs [r][k] = the first top_k tokens of that order.
  *  - logits: `dtype` XLPK_DTYPE_FP32 or XLPK_DTYPE_BF16, row r at logits_dev + r *
  *    row_stride elements, any alignment of the element type; arithmetic is fp32.
- *  - 0 <= top_k <= min(64, vocab); entropy_dev, rank_dev and, with top_k = 0, the
- *    top pointers may be NULL.
+ *  - vocab <= 2^30 and top_k <= 64 (else XLPK_ERR_UNSUPPORTED), 0 <= top_k <=
+ *    vocab; entropy_dev, rank_dev and, with top_k = 0, the top pointers may be
+ *    NULL.
  *  - Masked tokens are -inf (or the type's lowest value): probability 0.  A row of
  *    nothing but -inf has logprob and top_logprobs -inf and entropy 0.  A row with
  *    +inf or NaN has NaN for all of them (NaN sorts before +inf).

@@ -1,5 +1,40 @@
 // xlpk_decode_attention: attention of one new token per sequence over its KV
 // cache (include/xlpk.h has the definition).
+//
+// Mathematics.  Over the visible positions t in any order and grouping, with
+// running m = max s_t, l = sum 2^(s_t - m), o = sum 2^(s_t - m) v_t (s in units
+// of log 2): two groups join as m = max(m1, m2), l = l1 2^(m1-m) + l2 2^(m2-m),
+// o alike; out = o / l, lse = (m + log2 l) ln 2.  A tile is 16 positions; a warp
+// takes two at a time, keeps m, l and o of up to 16 query heads in registers and
+// joins with others only where its stretch of a segment (one kv head of one
+// sequence) ends.
+//
+// Bound.  Each K and V entry is read once and meets n_q / n_kv query heads: 4 to
+// 14 flop a byte, far below the tensor cores' ridge, so the floor is the cache's
+// bytes at HBM rate.  One long sequence comes to 91% of the copy rate (131072
+// positions of 8 kv heads of 128, bf16: 91 us for 537 MB).  What keeps shorter
+// ones from it is fixed: about 4 us from launch to the first data and 3.5 us for
+// the join.  e4m3 halves the bytes and not the work: each code is widened to
+// fp16 by a conversion and the loop issues 420 instructions for a tile of 4 KB,
+// so it runs at 70% of that rate (four of 131072, d 128: 236 us for 1.07 GB).
+//
+// Precision.  m16n8k16 MMAs with fp32 sums.  Cache entries are exact operands
+// (bf16, or e4m3 widened to fp16); q and p are split into as many 16-bit terms as
+// their type needs: one for a bf16 q, three of bf16 or two of fp16 for an fp32
+// q, two (three with fp32 output) for p, so that p's rounding stays far below
+// the output's.  With up to 8 heads a group the second term sits in rows 8-15 of
+// the A operand and costs no MMA.  The scores never leave registers: the C
+// fragment of q.k is the A fragment of p.v.
+//
+// Layout.  A K row is multiplied through a permutation of its dims that lets a
+// lane's 16 bytes of it be its B fragments as they are; likewise e4m3 V.  So a
+// lane reads only what it copied itself (cp.async, a queue of 16-byte chunks in
+// shared memory) and the loop has no barrier.  bf16 V goes through ldmatrix.trans
+// instead, which spares the byte permutation of each pair of its rows.
+//
+// Why mma.sync: a tile's contraction is 4 to 16 query rows wide; tcgen05 starts
+// at 64 rows and keeps sums in tensor memory, from which the scores would have
+// to come back for the softmax.  The tensor pipe is active a quarter of the time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -21,8 +56,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinWarps = 8;
 constexpr int kThreads = kJoinWarps * 32;   // of the join
-constexpr int kMaxCtas = 160;
-constexpr int kPieces = 4;
+constexpr int kMaxCtas = 160;               // one for each SM
+constexpr int kPieces = 4;                  // that warps as workers may cut a segment into, about
 constexpr int kTile = 16;   // positions of a tile; a warp takes two of its tiles at a time
 
 struct Args {
@@ -30,7 +65,7 @@ struct Args {
   float* parts;     // [workers][2] slots of partial results
   int ctas;         // of the attention
   int page_shift;   // log2 of page_size, or -1
-  bool flat;        // a tile never crosses a page
+  bool flat;        // the visible rows of a tile are in one page
   int4* joins;      // [workers] (sequence, kv head, last worker, -) of the segment that a worker begins and another ends; .x < 0: none
   int* team;        // warps of a worker
 };
@@ -127,12 +162,12 @@ __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                            bool f16) {
   if (f16)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // The next 16-bit term of x and y as a register; x and y keep the remainders.
@@ -919,6 +954,7 @@ xlpk_status launch(const Args& args, int ctas, cudaStream_t st) {
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   attention_kernel<S><<<ctas, S::THREADS, S::SMEM, st>>>(args);
+  XLPK_CUDA(cudaGetLastError());
   cudaLaunchConfig_t c{};
   const int group = args.a.n_q_heads / args.a.n_kv_heads;
   c.gridDim = dim3(std::max(ctas * group, (ctas * S::WARPS * group + kJoinWarps - 1) / kJoinWarps));
@@ -965,7 +1001,7 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   Args args;
   args.a = *a;
   args.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz(a->page_size) : -1;
-  args.flat = a->page_size % kTile == 0;
+  args.flat = a->page_size % kTile == 0 || a->table_cols == 1;   // (behind its only page no position is visible)
   args.ctas = std::min(sms, kMaxCtas);
   args.joins = static_cast<int4*>(workspace_dev);
   args.team = reinterpret_cast<int*>(args.joins + kMaxWorkers);

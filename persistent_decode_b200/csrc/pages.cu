@@ -3,8 +3,16 @@
 //
 // A call is a plan (one CTA: who keeps which page, which free pages are taken)
 // and, where bytes move, an apply launch of many CTAs that copies pages and
-// rewrites the table.  The plan is the only reader of `refs` as they were, so
-// fresh pages never depend on the order in which counts change.
+// rewrites the table; it is set up while the plan runs.  The plan alone reads
+// `refs` as they were, so fresh pages never depend on the order in which counts
+// change.
+//
+// Bound: small calls by the two launches (8 rows forked: 3.9 us on the device),
+// large ones by the bytes copied, each read and written once.  Copies use plain
+// 16-byte loads, four in flight a thread and eight CTAs an SM: compacting 54 pages of
+// 8.4 MB takes 165 us, of which the bytes are 140 at copy rate; 31 copies of a
+// page filled to 40 of 64 positions, in runs of 10 KB, 55 us of 50 (4 to 16 loads
+// and 2 to 8 CTAs: the same within 4% for whole pages, 4 to 57% slower for runs).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -433,6 +441,7 @@ xlpk_status xlpk_pages_fork(const xlpk_page_pool* p, const int32_t* parents_dev,
   XLPK_TRY(current_sms(&sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(*p, parents_dev, ws);
+  XLPK_CUDA(cudaGetLastError());
   const int table_blocks = (p->cols + kTableCols - 1) / kTableCols;
   return launch_after(fork_apply_kernel, table_blocks + sms * kCopyCtas, p->rows * kTableCols * 4, st, *p, parents_dev, ws,
                       table_blocks);
@@ -469,6 +478,7 @@ xlpk_status xlpk_pages_compact(const xlpk_page_pool* p, int32_t* remap_dev, void
   XLPK_TRY(current_sms(&sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(*p, remap_dev, ws);
+  XLPK_CUDA(cudaGetLastError());
   const long long n = static_cast<long long>(p->rows) * p->cols;
   const int table_blocks = static_cast<int>(std::min<long long>(sms, (n + kCopyThreads - 1) / kCopyThreads));
   return launch_after(compact_apply_kernel, table_blocks + sms * kCopyCtas, 0, st, *p, remap_dev, ws, table_blocks);
