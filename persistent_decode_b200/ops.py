@@ -79,46 +79,30 @@ _strided = getattr(_guards, "_empty_strided_cuda", None) or (
     lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
 
 
-def _empty(size, dtype):
-    """An uninitialised contiguous tensor of a tuple's size, on the current device."""
+def _contiguous(size):
+    """Strides of a contiguous tensor of a tuple's size."""
     stride, n = [1] * len(size), 1
     for i in range(len(size) - 1, -1, -1):
         stride[i] = n
-        n *= max(size[i], 1)
-    return _strided(size, tuple(stride), dtype)
+        n *= size[i] or 1
+    return tuple(stride)
 
 
-def _ptr(t) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
-class _On:
-    """The stream a call launches on: its allocations belong to it, and so, for an
-    explicit stream, do the tensors it uses, until that use is over."""
-    __slots__ = ("scope", "handle")
-
-    def __init__(self, device: int, stream, tensors):
-        if stream is None:
-            self.scope = None if torch.cuda.current_device() == device else torch.cuda.device(device)
-        else:
-            if stream.device.index != device:
-                _refuse(f"stream is on {stream.device}, the tensors on cuda:{device}")
-            self.scope = torch.cuda.stream(stream)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-            self.handle = stream.cuda_stream
-        if stream is None:
-            self.handle = torch._C._cuda_getCurrentRawStream(device)
-
-    def __enter__(self):
-        if self.scope is not None:
-            self.scope.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.scope is not None:
-            self.scope.__exit__(*exc)
+def _on(device: int, stream, tensors, launch):
+    """launch(handle) on the stream: its allocations belong to that stream, and so, for
+    an explicit one, do the tensors it uses, until that use is over."""
+    if stream is None:
+        if torch._C._cuda_getDevice() == device:
+            return launch(torch._C._cuda_getCurrentRawStream(device))
+        with torch.cuda.device(device):
+            return launch(torch._C._cuda_getCurrentRawStream(device))
+    if stream.device.index != device:
+        _refuse(f"stream is on {stream.device}, the tensors on cuda:{device}")
+    with torch.cuda.stream(stream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return launch(stream.cuda_stream)
 
 
 # ---- attention
@@ -189,36 +173,37 @@ def decode_attention(q, k_cache, v_cache, seq_lens, page_table=None, *, k_new=No
         _tensor(status, "status", 1, _I32, dev)
         if status.shape[0] < 1:
             _refuse("status must hold one int32")
-    with _On(dev, stream, (q, k_cache, v_cache, seq_lens, page_table, k_new, v_new, out, status)) as handle:
-        if out is None:
-            out = _empty((B, H, D), q.dtype)
-        lse = _empty((B, H), torch.float32) if return_lse else None
-        os = out.stride()
+    key = (KH > 0 and H > 8 * KH, D)
+
+    def launch(handle):
+        o = _strided((B, H, D), (H * D, D, 1), q.dtype) if out is None else out
+        os = o.stride()
+        lse = _strided((B, H), (H, 1), torch.float32) if return_lse else None
         try:
             args = _ATTENTION.pack(
-                q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), table_at, seq_lens.data_ptr(), out.data_ptr(),
-                _ptr(lse), _ptr(status),
+                q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), table_at, seq_lens.data_ptr(), o.data_ptr(),
+                0 if lse is None else lse.data_ptr(), 0 if status is None else status.data_ptr(),
                 0 if one_b else qs[0], 0 if one_h else qs[1],
                 0 if one_b else nk0, 0 if one_kh else nk1, 0 if one_b else nv0, 0 if one_kh else nv1,
                 0 if one_b else os[0], 0 if one_h else os[1],
                 0 if one_p else ks[0], 0 if one_kh else ks[1], 0 if one_pos else ks[2],
                 0 if one_p else vs[0], 0 if one_kh else vs[1], 0 if one_pos else vs[2], table_step,
-                B, H, KH, D, n_pages, P, cols, _IO[q.dtype], _KV[k_cache.dtype],
-                _int32(window, "window"), _int32(sinks, "sinks"),
+                B, H, KH, D, n_pages, P, cols, _IO[q.dtype], _KV[k_cache.dtype], window, sinks,
                 D ** -0.5 if scale is None else scale, k_scale, v_scale)
         except (struct.error, OverflowError, TypeError) as e:
-            raise ValueError(f"scale, k_scale or v_scale: {e}") from None
-        key = (KH > 0 and H > 8 * KH, D)
+            raise ValueError(f"window, sinks, scale, k_scale or v_scale: {e}") from None
         need = _WORKSPACE.get(key)
         if need is None:
             need = _fn("xlpk_decode_attention_workspace")(args)
             if need:
                 _WORKSPACE[key] = need
-        ws = _empty((max(need, 16),), torch.uint8)
+        ws = _strided((need or 16,), (1,), torch.uint8)
         st = _fn("xlpk_decode_attention")(args, ws.data_ptr(), need, handle)
         if st:
             _check(st, "xlpk_decode_attention")
-    return (out, lse) if return_lse else out
+        return (o, lse) if return_lse else o
+
+    return _on(dev, stream, (q, k_cache, v_cache, seq_lens, page_table, k_new, v_new, out, status), launch)
 
 
 # ---- pages
@@ -266,44 +251,44 @@ class PagePool:
     def device(self):
         return self.k.device
 
-    def _uses(self, *more):
-        return (self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status, *more)
-
-    def _workspace(self):
-        n = _fn("xlpk_pages_workspace")(self._c)
-        return _empty((max(n, 16),), torch.uint8), n
-
     def _per_row(self, t, name: str) -> int:
         _tensor(t, name, 1, _I32, self._device)
         if t.shape[0] != self._rows_n or not t.is_contiguous():
             _refuse(f"{name} must be a contiguous [rows]")
         return t.data_ptr()
 
+    def _call(self, name: str, stream, more, *args, workspace: bool = False) -> None:
+        def launch(handle):
+            if workspace:
+                n = _fn("xlpk_pages_workspace")(self._c)
+                ws = _strided((n or 16,), (1,), torch.uint8)
+                st = _fn(name)(self._c, *args, ws.data_ptr(), n, handle)
+            else:
+                st = _fn(name)(self._c, *args, handle)
+            if st:
+                _check(st, name)
+        if stream is None:
+            _on(self._device, None, (), launch)
+        else:
+            _on(self._device, stream, (self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status, *more), launch)
+
     def fork(self, parents, stream=None) -> None:
         """xlpk_pages_fork: row r becomes what row parents[r] was (-1: empty); `parents` int32 [rows]."""
-        at = self._per_row(parents, "parents")
-        with _On(self._device, stream, self._uses(parents)) as handle:
-            ws, n = self._workspace()
-            _check(_fn("xlpk_pages_fork")(self._c, at, ws.data_ptr(), n, handle), "xlpk_pages_fork")
+        self._call("xlpk_pages_fork", stream, (parents,), self._per_row(parents, "parents"), workspace=True)
 
     def reserve(self, want, stream=None) -> None:
         """xlpk_pages_reserve: pages so that row r can hold want[r] positions; `want` int32 [rows]."""
-        at = self._per_row(want, "want")
-        with _On(self._device, stream, self._uses(want)) as handle:
-            _check(_fn("xlpk_pages_reserve")(self._c, at, handle), "xlpk_pages_reserve")
+        self._call("xlpk_pages_reserve", stream, (want,), self._per_row(want, "want"))
 
     def trim(self, window: int, sinks: int = 0, stream=None) -> None:
         """xlpk_pages_trim: give back the pages a sliding window has passed."""
-        with _On(self._device, stream, self._uses()) as handle:
-            _check(_fn("xlpk_pages_trim")(self._c, _int32(window, "window"), _int32(sinks, "sinks"), handle), "xlpk_pages_trim")
+        self._call("xlpk_pages_trim", stream, (), _int32(window, "window"), _int32(sinks, "sinks"))
 
     def compact(self, stream=None):
         """xlpk_pages_compact: move the live pages to the lowest numbers; returns the new
         number of every page, int32 [n_pages] (-1: free)."""
-        with _On(self._device, stream, self._uses()) as handle:
-            remap = _empty((self.refs.shape[0],), torch.int32)
-            ws, n = self._workspace()
-            _check(_fn("xlpk_pages_compact")(self._c, remap.data_ptr(), ws.data_ptr(), n, handle), "xlpk_pages_compact")
+        remap = _on(self._device, stream, (), lambda _: _strided((self.refs.shape[0],), (1,), torch.int32))
+        self._call("xlpk_pages_compact", stream, (), remap.data_ptr(), workspace=True)
         return remap
 
     def copy(self, src, dst, stream=None) -> None:
@@ -312,9 +297,7 @@ class PagePool:
         n = len(src)
         if len(dst) != n:
             _refuse("src and dst of different lengths")
-        with _On(self._device, stream, self._uses()) as handle:
-            _check(_fn("xlpk_pages_copy")(self._c, (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n, handle),
-                   "xlpk_pages_copy")
+        self._call("xlpk_pages_copy", stream, (), (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n)
 
     def check(self) -> None:
         """Waits for the calls so far; raises what stopped one of them, and lets the pool go on."""
@@ -356,15 +339,23 @@ def token_logprobs(logits, tokens, top_k: int = 0, stream=None) -> TokenLogprobs
             x = logits.view(rows, vocab)
         except RuntimeError:
             _refuse("the leading dimensions of logits must step evenly")
-    with _On(dev, stream, (logits, tokens)) as handle:
+    f32, i32 = torch.float32, torch.int32
+
+    def launch(handle):
         shape = tuple(tokens.shape)
-        logprob, entropy, rank = _empty(shape, torch.float32), _empty(shape, torch.float32), _empty(shape, torch.int32)
+        stride = _contiguous(shape)
+        logprob, entropy, rank = _strided(shape, stride, f32), _strided(shape, stride, f32), _strided(shape, stride, i32)
         top_ids = top = None
+        ids_at = top_at = 0
         if top_k > 0:
-            top_ids, top = _empty((*shape, top_k), torch.int32), _empty((*shape, top_k), torch.float32)
+            shape, stride = (*shape, top_k), (*[n * top_k for n in stride], 1)
+            top_ids, top = _strided(shape, stride, i32), _strided(shape, stride, f32)
+            ids_at, top_at = top_ids.data_ptr(), top.data_ptr()
         st = _fn("xlpk_token_logprobs")(
             x.data_ptr(), _IO[x.dtype], rows, vocab, x.stride(0) if rows > 1 else 0, tokens.data_ptr(), top_k,
-            logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), _ptr(top_ids), _ptr(top), handle)
+            logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), ids_at, top_at, handle)
         if st:
             _check(st, "xlpk_token_logprobs")
-    return TokenLogprobs(logprob, entropy, rank, top_ids, top)
+        return TokenLogprobs(logprob, entropy, rank, top_ids, top)
+
+    return _on(dev, stream, (logits, tokens), launch)
