@@ -15,8 +15,8 @@
 // positions of 8 kv heads of 128, bf16: 91 us for 537 MB).  What keeps shorter
 // ones from it is fixed: about 4 us from launch to the first data and 3.5 us for
 // the join.  e4m3 halves the bytes and not the work: each code is widened to
-// fp16 by a conversion and the loop issues 420 instructions for a tile of 4 KB,
-// so it runs at 70% of that rate (four of 131072, d 128: 236 us for 1.07 GB).
+// fp16 by a conversion and the loop issues 334 instructions for a tile of 4 KB,
+// so it runs at 71% of that rate (four of 131072, d 128: 234 us for 1.07 GB).
 //
 // Precision.  m16n8k16 MMAs with fp32 sums.  Cache entries are exact operands
 // (bf16, or e4m3 widened to fp16); q and p are split into as many 16-bit terms as
