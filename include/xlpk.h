@@ -569,7 +569,8 @@ xlpk_status xlpk_pages_copy(const xlpk_page_pool* pool, const int32_t* src_host,
  *  - vocab <= 2^30 and top_k <= 64 (else XLPK_ERR_UNSUPPORTED), 0 <= top_k <=
  *    vocab; entropy_dev, rank_dev and, with top_k = 0, the top pointers may be
  *    NULL.
- *  - Masked tokens are -inf (or the type's lowest value): probability 0.  A row of
+ *  - Masked tokens are -inf, or a finite value far below the others (down to the
+ *    type's lowest): probability 0.  A row of
  *    nothing but -inf has logprob and top_logprobs -inf and entropy 0.  A row with
  *    +inf or NaN has NaN for all of them (NaN sorts before +inf).
  *  - A token outside [0, vocab) (padding) gives logprob NaN and rank -1. */

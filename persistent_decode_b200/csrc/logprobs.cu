@@ -46,7 +46,10 @@ constexpr int kStages = 2;         // rounds on their way
 constexpr int kStep = kUnroll * kThreads;
 constexpr int kPushed = 512;       // candidates that are ranked at most
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kFar = 1e38f;      // a maximum this far out has no neighbour within 2^100: all others weigh 0
+// A maximum this far out has no neighbour within 64, so all others weigh less than 2^-92 and are left
+// out.  Nearer ones have a base, m log2(e) rounded, that is off by 64 at most, which exponentials of it
+// stand; further out what the rounding leaves is an exponent of its own (-1e10: 440).
+constexpr float kFar = 0x1p30f;
 
 // A logit's place in descending order: larger keys come first, NaN before +inf,
 // -0 equals +0; ties go to the lower index.  No value has key 0.

@@ -322,7 +322,8 @@ def token_logprobs(logits, tokens, top_k: int = 0, stream=None) -> TokenLogprobs
 
     `logits` [..., vocab] fp32 or bf16, as a decode writes them ([steps][B][vocab]),
     rows at any stride; `tokens` int32 of the leading shape.  top_k <= 64
-    alternatives, best first, ties by the lower id.  Masked logits are -inf.
+    alternatives, best first, ties by the lower id.  Masked logits are -inf, or finite
+    and far below the others.
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() < 1 or logits.dtype not in _IO or not logits.is_cuda:
         _refuse("logits must be an fp32 or bf16 CUDA tensor [..., vocab]")

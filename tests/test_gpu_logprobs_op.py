@@ -136,6 +136,36 @@ def test_nan_nearly_everywhere(cuda_device, dtype):
     check(x, [101, 8999], run(x, [101, 8999], 64), 64)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("low", [-1e4, -1e9, -3e9, -1e10, -1e12, -1e15, -1e30, -2e30, -1e35, -1e38])
+def test_masks_of_finite_values(cuda_device, low, dtype):
+    # masks that are neither -inf nor the type's lowest value; they are so far below the others, and
+    # so far from each other, that their weights are exactly 0 in 64 bits too
+    V, g = 40000, torch.Generator().manual_seed(12)
+    base = (torch.randn(V, generator=g) * 2).to(dtype)
+    rows = []
+
+    def row(f):
+        x = base.clone()
+        f(x)
+        rows.append(x)
+
+    row(lambda x: x.fill_(low))                                  # nothing else is left: uniform
+    row(lambda x: x[:-1].fill_(low))                             # the last token alone
+    row(lambda x: x[1:].fill_(low))
+    row(lambda x: x[:V // 2].fill_(low))                         # whole rounds of every thread, then the others
+    row(lambda x: x[V // 2:].fill_(low))
+    row(lambda x: x[::2].fill_(low))
+    row(lambda x: x.copy_(torch.where(torch.rand(V, generator=g) < 0.999, low, base.float()).to(dtype)))
+    row(lambda x: x.copy_((low * (1 + torch.arange(V) % 3)).to(dtype)))     # masked more than once: uniform over every third
+    row(lambda x: x[7].fill_(-low))                              # as far out on the other side
+    row(lambda x: x.copy_((-low * (1 + torch.arange(V) // 5000)).to(dtype)))
+    x = torch.stack(rows)
+    for tok in ([0] * len(rows), [V - 1] * len(rows), [7] * len(rows)):
+        check(x, tok, run(x, tok, 0), 0)
+    check(x, tok, run(x, tok, 64), 64)
+
+
 def test_a_certain_token_keeps_its_small_logprob(cuda_device):
     # log p of the best token is -s with s = 9 e^-20: far below the step of 1, kept to relative 2^-13
     x = torch.zeros(1, 10)
