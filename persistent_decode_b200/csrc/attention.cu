@@ -817,9 +817,11 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
     if (begins && !ends && rank == 0 && lane == 0) {
       args.joins[worker] = make_int4(w.b, w.h, shares.owner(x + w.s.tiles - 1), 0);
     }
-    if (team == 1) __syncwarp();   // the scratch has been read
     x += w.end - w.i;
     if (w.left == 0) break;
+    // All of the worker's warps have read the scratch: one of them may be done with the next segment, and
+    // write its maximum and sum there, before a slower one is done with this.
+    worker_sync();
     walk_next(a, w);
   }
 }

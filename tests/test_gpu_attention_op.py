@@ -167,6 +167,19 @@ def test_one_sequence_outlasts_all_others(cuda_device):
     check(s, *call(s))
 
 
+@pytest.mark.parametrize("H,KH,D,kv,io", [(16, 1, 128, "bf16", torch.float32), (16, 1, 128, "e4m3", torch.bfloat16),
+                                          (9, 1, 64, "e4m3", torch.float32), (8, 1, 128, "bf16", torch.bfloat16)])
+def test_short_segments_follow_each_other_in_one_cta(cuda_device, H, KH, D, kv, io):
+    # one long sequence makes CTAs the workers; each of them then joins its warps' results for a dozen
+    # segments of one tile, through the same scratch, one right after the other
+    s = make(1500, [30000] + [1 + b % 16 for b in range(1499)], H, KH, D, 16, kv, io, seed=22)
+    got, lse = call(s)
+    check(s, got, lse)
+    for _ in range(10):
+        a, b = call(s)
+        assert torch.equal(a, got) and torch.equal(b, lse)
+
+
 def test_ragged_lengths_share_the_work(cuda_device):
     lens = [5, 9000, 0, 1, 333, 0, 2500, 16]
     s = make(len(lens), lens, 8, 2, 128, 64, "e4m3", torch.float32, seed=3)
