@@ -267,10 +267,14 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const xlpk_page_p
 // ---- trim
 
 __global__ void __launch_bounds__(kCopyThreads) trim_kernel(const xlpk_page_pool p, int window, int sinks) {
-  if (*p.status_dev != XLPK_OK) return;
   const long long cap = static_cast<long long>(p.cols) * p.page_size;
-  int bad = 0;
+  // Every CTA looks at all lengths and comes to the same answer; the first says it.  (It may do so while
+  // others still read the status: one that some of a CTA's threads see set stops all of them, none early,
+  // so that no thread's lengths go unlooked at.)
+  const bool stopped = *p.status_dev != XLPK_OK;
+  bool bad = false;
   for (int r = threadIdx.x; r < p.rows; r += kCopyThreads) bad |= p.seq_lens_dev[r] < 0 || p.seq_lens_dev[r] > cap;
+  if (__syncthreads_or(stopped)) return;
   if (__syncthreads_or(bad)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status_dev = XLPK_ERR_INVALID_ARG;
     return;

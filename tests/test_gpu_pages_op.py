@@ -298,6 +298,34 @@ def test_what_cannot_be_done_changes_nothing_and_stops_the_pool(cuda_device, wha
     assert not unchanged(p, snap)
 
 
+@pytest.mark.parametrize("row", [0, 255, 256, 511, 700, 999])
+def test_trim_of_a_large_table_changes_all_or_nothing(cuda_device, row):
+    # a table of hundreds of CTAs' work with one bad length: whichever thread looks at it, and however
+    # late a CTA starts, nothing is trimmed; with the length put right everything behind the window is
+    rows, cols, P, pages = 1000, 600, 2, 64
+    g = torch.Generator().manual_seed(row)
+    table = torch.randint(0, pages, (rows, cols), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, cols * P + 1, (rows,), generator=g, dtype=torch.int32)
+    k = torch.zeros((1, pages, 1, P, 64), dtype=torch.bfloat16, device=cuda_device)
+    p = PagePool(k, k.clone(), table.cuda(), lens.cuda())
+    snap = snapshot(p)
+    for bad in (-1, cols * P + 1) * 10:
+        p.seq_lens[row] = bad
+        p.trim(100, 7)
+        with pytest.raises(XlpkError) as e:
+            p.check()
+        assert e.value.status == _abi.XLPK_ERR_INVALID_ARG
+        p.seq_lens[row] = lens[row]
+        assert unchanged(p, snap)
+    p.trim(100, 7)
+    p.check()
+    j = torch.arange(cols)
+    gone = ((j + 1) * P <= lens[:, None] - 100) & (j * P >= 7)
+    want = torch.where(gone, -1, table)
+    assert torch.equal(p.page_table.cpu(), want)
+    assert torch.equal(p.refs.cpu(), torch.bincount(want[want >= 0].long(), minlength=pages).int())
+
+
 def test_captured_and_replayed(cuda_device):
     h, p = make(4, 6, 8, 40, [20, 9, 0, 31], seed=10)
     parents, want = i32([0, 0, 1, 3]), i32([24, 24, 16, 32])
