@@ -262,7 +262,8 @@ class Engine:
     def page_pool(self, seq_lens, refs=None):
         """The paged cache's ops.PagePool: `seq_lens` int32 CUDA tensor [B] of positions
         in the cache.  Its calls change the table that later decodes read; name the
-        lengths they left to set_state."""
+        lengths they left to set_state.  (A table or pools that are assigned to it are
+        not the engine's.)"""
         from .ops import PagePool
         _, k, v, table = self._refs
         if table is None:

@@ -214,26 +214,31 @@ class PagePool:
     `k`, `v` [L][n_pages][n_kv][page_size][d] as the engine's pools; `page_table`
     int32 [rows][cols] (-1: no page), `seq_lens` int32 [rows], `refs` int32
     [n_pages] (None: counted from the table; the caller may add references of its
-    own).  All stay the caller's and are updated in place.  Calls are
+    own).  All stay the caller's and are updated in place; the attributes of these
+    names may be assigned other tensors, which later calls then use.  Calls are
     asynchronous; one that cannot be done changes nothing and sets `status`
     (int32 [1]), which stops later calls until `check()` has reported it.
     """
 
     def __init__(self, k, v, page_table, seq_lens, refs=None, status=None):
         _tensor(k, "k", 5, _KV, -1)
-        dev = k.get_device()
-        _tensor(v, "v", 5, (k.dtype,), dev)
-        _tensor(page_table, "page_table", 2, _I32, dev)
-        _tensor(seq_lens, "seq_lens", 1, _I32, dev)
-        L, n_pages, KH, P, D = k.shape
+        _tensor(page_table, "page_table", 2, _I32, k.get_device())
         if refs is None:
-            held = page_table.reshape(-1)
+            held, n_pages = page_table.reshape(-1), k.shape[1]
             held = held[(held >= 0) & (held < n_pages)]
             refs = torch.bincount(held, minlength=n_pages).to(torch.int32)
         if status is None:
             status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        _tensor(refs, "refs", 1, _I32, dev)
-        _tensor(status, "status", 1, _I32, dev)
+        self._bind(k, v, page_table, seq_lens, refs, status)
+
+    def _bind(self, k, v, page_table, seq_lens, refs, status) -> None:
+        """Takes the six tensors, all of them or (ValueError) none."""
+        _tensor(k, "k", 5, _KV, -1)
+        dev = k.get_device()
+        _tensor(v, "v", 5, (k.dtype,), dev)
+        for t, name, dim in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1), (refs, "refs", 1), (status, "status", 1)):
+            _tensor(t, name, dim, _I32, dev)
+        L, n_pages, KH, P, D = k.shape
         rows, cols = page_table.shape
         if v.shape != k.shape:
             _refuse(f"pools of {tuple(k.shape)} and {tuple(v.shape)}")
@@ -242,22 +247,33 @@ class PagePool:
         if not (k.is_contiguous() and v.is_contiguous() and page_table.is_contiguous() and seq_lens.is_contiguous()
                 and refs.is_contiguous()):
             _refuse("pool tensors must be contiguous")
-        self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status = k, v, page_table, seq_lens, refs, status
-        self._device, self._rows_n = dev, rows
-        self._c = _POOL.pack(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
-                             status.data_ptr(), L, n_pages, KH, P, D * k.element_size(), rows, cols)
+        held = (k, v, page_table, seq_lens, refs, status)
+        at = tuple([t.data_ptr() for t in held])
+        try:
+            c = _POOL.pack(*at, L, n_pages, KH, P, D * k.element_size(), rows, cols)
+        except struct.error as e:
+            raise ValueError(f"a size does not fit an int32: {e}") from None
+        self._held, self._at, self._c, self._device, self._rows_n, self._pages_n = held, at, c, dev, rows, n_pages
+
+    # The tensors may be assigned, and are checked again then (`pool.seq_lens += 1` assigns too).
+    k, v, page_table, seq_lens, refs, status = (
+        property(lambda self, i=i: self._held[i],
+                 lambda self, t, i=i: self._bind(*self._held[:i], t, *self._held[i + 1:])) for i in range(6))
 
     @property
     def device(self):
         return self.k.device
 
-    def _per_row(self, t, name: str) -> int:
-        _tensor(t, name, 1, _I32, self._device)
-        if t.shape[0] != self._rows_n or not t.is_contiguous():
-            _refuse(f"{name} must be a contiguous [rows]")
-        return t.data_ptr()
+    def _call(self, name: str, stream, *args, row=None, row_name: str = "", workspace: bool = False) -> None:
+        """`row`: the call's first argument, an int32 tensor of one entry a row."""
+        if tuple([t.data_ptr() for t in self._held]) != self._at:   # one was given other memory (t.data = ..., resize_)
+            self._bind(*self._held)
+        if row_name:
+            _tensor(row, row_name, 1, _I32, self._device)
+            if row.shape[0] != self._rows_n or not row.is_contiguous():
+                _refuse(f"{row_name} must be a contiguous [rows]")
+            args = (row.data_ptr(), *args)
 
-    def _call(self, name: str, stream, more, *args, workspace: bool = False) -> None:
         def launch(handle):
             if workspace:
                 n = _fn("xlpk_pages_workspace")(self._c)
@@ -267,28 +283,25 @@ class PagePool:
                 st = _fn(name)(self._c, *args, handle)
             if st:
                 _check(st, name)
-        if stream is None:
-            _on(self._device, None, (), launch)
-        else:
-            _on(self._device, stream, (self.k, self.v, self.page_table, self.seq_lens, self.refs, self.status, *more), launch)
+        _on(self._device, stream, () if stream is None else (*self._held, row), launch)
 
     def fork(self, parents, stream=None) -> None:
         """xlpk_pages_fork: row r becomes what row parents[r] was (-1: empty); `parents` int32 [rows]."""
-        self._call("xlpk_pages_fork", stream, (parents,), self._per_row(parents, "parents"), workspace=True)
+        self._call("xlpk_pages_fork", stream, row=parents, row_name="parents", workspace=True)
 
     def reserve(self, want, stream=None) -> None:
         """xlpk_pages_reserve: pages so that row r can hold want[r] positions; `want` int32 [rows]."""
-        self._call("xlpk_pages_reserve", stream, (want,), self._per_row(want, "want"))
+        self._call("xlpk_pages_reserve", stream, row=want, row_name="want")
 
     def trim(self, window: int, sinks: int = 0, stream=None) -> None:
         """xlpk_pages_trim: give back the pages a sliding window has passed."""
-        self._call("xlpk_pages_trim", stream, (), _int32(window, "window"), _int32(sinks, "sinks"))
+        self._call("xlpk_pages_trim", stream, _int32(window, "window"), _int32(sinks, "sinks"))
 
     def compact(self, stream=None):
         """xlpk_pages_compact: move the live pages to the lowest numbers; returns the new
         number of every page, int32 [n_pages] (-1: free)."""
-        remap = _on(self._device, stream, (), lambda _: _strided((self.refs.shape[0],), (1,), torch.int32))
-        self._call("xlpk_pages_compact", stream, (), remap.data_ptr(), workspace=True)
+        remap = _on(self._device, stream, (), lambda _: _strided((self._pages_n,), (1,), torch.int32))
+        self._call("xlpk_pages_compact", stream, remap.data_ptr(), workspace=True)
         return remap
 
     def copy(self, src, dst, stream=None) -> None:
@@ -297,7 +310,7 @@ class PagePool:
         n = len(src)
         if len(dst) != n:
             _refuse("src and dst of different lengths")
-        self._call("xlpk_pages_copy", stream, (), (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n)
+        self._call("xlpk_pages_copy", stream, (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n)
 
     def check(self) -> None:
         """Waits for the calls so far; raises what stopped one of them, and lets the pool go on."""

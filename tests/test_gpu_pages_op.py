@@ -326,6 +326,49 @@ def test_trim_of_a_large_table_changes_all_or_nothing(cuda_device, row):
     assert torch.equal(p.refs.cpu(), torch.bincount(want[want >= 0].long(), minlength=pages).int())
 
 
+def test_assigned_tensors_are_used_and_bad_ones_refused(cuda_device):
+    h, p = make(4, 6, 8, 40, [20, 9, 0, 31], seed=20)
+    p.seq_lens = p.seq_lens + 1                    # the tensor before has no owner any more:
+    others = [torch.full((4,), -7, dtype=torch.int32, device=cuda_device) for _ in range(64)]   # its memory is theirs
+    h.lens = [n + 1 for n in h.lens]
+    h.reserve([21, 10, 1, 32])
+    p.reserve(i32([21, 10, 1, 32]))
+    p.check()
+    same(h, p)
+    p.page_table, p.refs = p.page_table.clone(), p.refs.clone()
+    p.k, p.v = p.k.clone(), p.v.clone()
+    p.status = torch.zeros(3, dtype=torch.int32, device=cuda_device)
+    others += [torch.full_like(t, -7) for t in (p.page_table, p.refs) for _ in range(16)]
+    h.fork([0, 0, 1, 3])
+    p.fork(i32([0, 0, 1, 3]))
+    assert p.compact().tolist() == h.compact()
+    p.check()
+    same(h, p)
+    p.seq_lens += 1                                # in place, and assigned
+    p.refs[:1] += 0
+    h.lens = [n + 1 for n in h.lens]
+    same(h, p)
+    p.seq_lens.data = p.seq_lens.clone()           # the same tensor at another address
+    others += [torch.full((4,), -7, dtype=torch.int32, device=cuda_device) for _ in range(64)]
+    h.reserve([30, 30, 30, 40])
+    p.reserve(i32([30, 30, 30, 40]))
+    p.check()
+    same(h, p)
+    for t in others:
+        assert bool((t == -7).all())
+    for name, bad in (("seq_lens", p.seq_lens[:3]), ("seq_lens", p.seq_lens.long()), ("seq_lens", p.seq_lens.cpu()), ("seq_lens", None),
+                      ("page_table", p.page_table[:2]), ("page_table", p.page_table[:, ::2]), ("refs", p.refs[:5]),
+                      ("k", p.k[:, :4]), ("v", p.v.view(torch.uint8)), ("status", p.status[:0])):
+        was = getattr(p, name)
+        with pytest.raises(ValueError):
+            setattr(p, name, bad)
+        assert getattr(p, name) is was
+    h.fork([3, 0, 1, 3])
+    p.fork(i32([3, 0, 1, 3]))
+    p.check()
+    same(h, p)
+
+
 def test_captured_and_replayed(cuda_device):
     h, p = make(4, 6, 8, 40, [20, 9, 0, 31], seed=10)
     parents, want = i32([0, 0, 1, 3]), i32([24, 24, 16, 32])
