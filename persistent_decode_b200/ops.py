@@ -217,7 +217,8 @@ class PagePool:
     own).  All stay the caller's and are updated in place; the attributes of these
     names may be assigned other tensors, which later calls then use.  Calls are
     asynchronous; one that cannot be done changes nothing and sets `status`
-    (int32 [1]), which stops later calls until `check()` has reported it.
+    (int32 [1]), which stops later calls until `check()` has reported it.  Calls on
+    several streams are the caller's to put in order, as with any tensor.
     """
 
     def __init__(self, k, v, page_table, seq_lens, refs=None, status=None):
@@ -229,6 +230,7 @@ class PagePool:
             refs = torch.bincount(held, minlength=n_pages).to(torch.int32)
         if status is None:
             status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._streams = {}     # handle -> stream of the calls so far, for check()
         self._bind(k, v, page_table, seq_lens, refs, status)
 
     def _bind(self, k, v, page_table, seq_lens, refs, status) -> None:
@@ -275,6 +277,8 @@ class PagePool:
             args = (row.data_ptr(), *args)
 
         def launch(handle):
+            if handle not in self._streams:
+                self._streams[handle] = torch.cuda.current_stream(self._device)
             if workspace:
                 n = _fn("xlpk_pages_workspace")(self._c)
                 ws = _strided((n or 16,), (1,), torch.uint8)
@@ -313,11 +317,23 @@ class PagePool:
         self._call("xlpk_pages_copy", stream, (C.c_int32 * n)(*src), (C.c_int32 * n)(*dst), n)
 
     def check(self) -> None:
-        """Waits for the calls so far; raises what stopped one of them, and lets the pool go on."""
-        st = int(self.status[0])
-        if st != _abi.XLPK_OK:
-            self.status[:1] = 0
-            raise XlpkError(st, "page pool", detail="the call that met it, and those after it, changed nothing")
+        """Waits for the calls so far, on whatever streams they were made; raises what stopped one
+        of them, and lets the pool go on.  (Replays of a captured graph are calls of the stream
+        that it was replayed on, which the caller has to wait for.)"""
+        with torch.cuda.device(self._device):
+            here = torch.cuda.current_stream()
+            for handle in [h for h in self._streams if h != here.cuda_stream]:
+                there = self._streams[handle]
+                with torch.cuda.stream(there):
+                    recording = torch.cuda.is_current_stream_capturing()   # what it records has not run
+                if not recording:
+                    here.wait_stream(there)
+                    del self._streams[handle]
+            st = int(self.status[0])
+            if st != _abi.XLPK_OK:
+                self.status[:1] = 0
+                here.synchronize()     # before any stream's next call
+                raise XlpkError(st, "page pool", detail="the call that met it, and those after it, changed nothing")
 
 
 # ---- log probabilities

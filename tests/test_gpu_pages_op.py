@@ -408,6 +408,58 @@ def test_on_another_stream(cuda_device):
     same(h, p)
 
 
+@pytest.mark.parametrize("how", ["argument", "context"])
+def test_check_waits_for_every_stream(cuda_device, how):
+    # calls on two side streams, each behind some milliseconds of other work, and no other synchronisation
+    h, p = make(4, 4, 8, 12, [20, 9, 0, 31], seed=13)
+    snap = snapshot(p)
+    busy = torch.randn(4096, 4096, device=cuda_device)
+    want = i32([32, 32, 32, 32])        # 5 pages lack, 3 are free
+    fits = i32([24, 16, 8, 32])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+
+    def reserve(st, w):
+        with torch.cuda.stream(st):
+            for _ in range(30):
+                torch.mm(busy, busy)
+            if how == "context":
+                p.reserve(w)
+        if how == "argument":
+            p.reserve(w, stream=st)
+
+    for bad in streams:
+        reserve(bad, want)
+        with pytest.raises(XlpkError) as e:
+            p.check()
+        assert e.value.status == _abi.XLPK_ERR_OOM
+        assert unchanged(p, snap)
+        p.check()
+    # the status is clear for the next call of another stream, which check() waits for as well
+    reserve(streams[0], fits)
+    p.check()
+    h.reserve([24, 16, 8, 32])
+    same(h, p)
+
+
+def test_check_while_another_stream_records(cuda_device):
+    h, p = make(3, 6, 8, 40, [20, 9, 31], seed=14)
+    p.fork(i32([0, 1, 2]))
+    st, parents = torch.cuda.Stream(), i32([2, 0, 2])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st):
+        g.capture_begin(capture_error_mode="relaxed")
+        p.fork(parents)
+    p.check()
+    with torch.cuda.stream(st):
+        g.capture_end()
+        g.replay()
+    p.check()              # (the graph was replayed on the stream that recorded it)
+    h.fork([2, 0, 2])
+    same(h, p)
+
+
 def test_offsets_past_32_bits(cuda_device):
     # one layer of K and V of more than 2^32 bytes each; pages at its end are copied, forked and moved to its start
     P, n = 1024, (1 << 32) // (1024 * 128) + 64
