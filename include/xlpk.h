@@ -549,7 +549,8 @@ xlpk_status xlpk_pages_trim(const xlpk_page_pool* pool, int32_t window, int32_t 
 /* Move the live pages (refs > 0) to the numbers below their count: the k-th
  * free page below it takes the contents of the k-th live page at or above it.
  * Table and counts follow.  remap_dev [n_pages] (or NULL): the new number of
- * every page, -1 for a free one, for references that the caller keeps. */
+ * every page, -1 for a free one, for references that the caller keeps (a call that
+ * is stopped by *status_dev writes the numbers that the pages have). */
 xlpk_status xlpk_pages_compact(const xlpk_page_pool* pool, int32_t* remap_dev, void* workspace_dev,
                                int64_t workspace_bytes, void* stream);
 

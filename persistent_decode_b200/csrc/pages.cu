@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const xlpk_p
   __shared__ int warp_sums[32];
   const CompactPlan c = compact_plan_at(ws, p.n_pages);
   int* remap = remap_dev ? remap_dev : c.remap;
-  if (*p.status_dev != XLPK_OK) {
+  if (*p.status_dev != XLPK_OK) {   // nothing moves: every live page keeps its number
+    for (int i = threadIdx.x; i < p.n_pages; i += kPlanThreads) remap[i] = p.refs_dev[i] > 0 ? i : -1;
     if (threadIdx.x == 0) *c.count = -1;
     return;
   }

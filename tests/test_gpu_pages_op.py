@@ -298,6 +298,21 @@ def test_what_cannot_be_done_changes_nothing_and_stops_the_pool(cuda_device, wha
     assert not unchanged(p, snap)
 
 
+def test_compact_of_a_stopped_pool_returns_the_numbers_that_pages_have(cuda_device):
+    h, p = make(4, 6, 8, 3000, [20, 9, 0, 31], L=1, seed=18)
+    snap = snapshot(p)
+    p.fork(i32([0, 0, 0, 9]))          # no such row
+    junk = torch.full((3000,), 12345, dtype=torch.int32, device=cuda_device)
+    del junk                           # what the result's memory may have held
+    remap = p.compact()
+    assert remap.tolist() == [i if c > 0 else -1 for i, c in enumerate(h.refs)]
+    assert unchanged(p, snap)
+    with pytest.raises(XlpkError):
+        p.check()
+    assert p.compact().tolist() == h.compact()
+    same(h, p)
+
+
 @pytest.mark.parametrize("row", [0, 255, 256, 511, 700, 999])
 def test_trim_of_a_large_table_changes_all_or_nothing(cuda_device, row):
     # a table of hundreds of CTAs' work with one bad length: whichever thread looks at it, and however
