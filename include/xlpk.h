@@ -397,6 +397,10 @@ xlpk_status xlpk_generate(xlpk_handle h, const int32_t* tokens_host, const int32
  * section 7.3, execution stability at the hardware's limits). */
 xlpk_status xlpk_get_status(xlpk_handle h);
 
+/* The steps that xlpk_decode would still take: the least max_seq - seq_len of the
+ * handle's sequences.  XLPK_ERR_INVALID_ARG while the serve loop owns the handle. */
+xlpk_status xlpk_get_room(xlpk_handle h, int32_t* n_steps);
+
 /* Facts about a created handle (grid, shared memory, ring, packed bytes).
  * (The pages are silent; measurement support.) */
 xlpk_status xlpk_get_info(xlpk_handle h, xlpk_info* out);

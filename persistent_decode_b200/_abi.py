@@ -114,6 +114,7 @@ SIGNATURES = {
     "xlpk_generate": (C.c_int32, [C.c_void_p, C.POINTER(C.c_int32), C.POINTER(C.c_int32), C.c_int32,
                                   C.POINTER(C.c_int32), C.c_void_p]),
     "xlpk_get_status": (C.c_int32, [C.c_void_p]),
+    "xlpk_get_room": (C.c_int32, [C.c_void_p, C.POINTER(C.c_int32)]),
     "xlpk_get_info": (C.c_int32, [C.c_void_p, C.POINTER(xlpk_info)]),
     "xlpk_status_string": (C.c_char_p, [C.c_int32]),
     "xlpk_last_cuda_error": (C.c_char_p, []),

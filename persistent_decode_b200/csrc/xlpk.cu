@@ -1640,6 +1640,14 @@ xlpk_status xlpk_get_status(xlpk_handle h) {
   return static_cast<xlpk_status>(st[0]);
 }
 
+xlpk_status xlpk_get_room(xlpk_handle h, int32_t* n_steps) {
+  if (!h || !n_steps || h->serve_active) return XLPK_ERR_INVALID_ARG;
+  int room = h->cfg.max_seq;
+  for (int b = 0; b < h->cfg.batch; ++b) room = std::min(room, h->cfg.max_seq - h->pos[b]);
+  *n_steps = room;
+  return XLPK_OK;
+}
+
 xlpk_status xlpk_get_info(xlpk_handle h, xlpk_info* out) {
   if (!h || !out) return XLPK_ERR_INVALID_ARG;
   out->n_ctas = h->G;

@@ -189,6 +189,12 @@ class Engine:
         _check(lib.xlpk_get_info(self.h, C.byref(out)), "xlpk_get_info")
         return out
 
+    def room(self) -> int:
+        """The steps that decode would still take before a sequence's cache is full."""
+        n = C.c_int32()
+        _check(lib.xlpk_get_room(self.h, C.byref(n)), "xlpk_get_room")
+        return int(n.value)
+
     def set_state(self, tokens, seq_lens, stream=None) -> None:
         t = (C.c_int32 * self.B)(*[int(v) for v in tokens])
         s = (C.c_int32 * self.B)(*[int(v) for v in seq_lens])
@@ -237,8 +243,9 @@ class Engine:
         """Log probabilities of given tokens: feed `tokens` (int32 CUDA tensor [n][B])
         after the pending ones, as a decode forced to them, and return their
         ops.TokenLogprobs ([n][B], alternatives [n][B][top_k]).  The state moves on by
-        n positions; the last tokens are pending.  Logits live in a buffer of at most
-        SCORE_BYTES (or one step), whatever n."""
+        n positions; the last tokens are pending.  A call that is refused (top_k, more
+        tokens than there is room for) leaves it where it was.  Logits live in a buffer of
+        at most SCORE_BYTES (or one step), whatever n."""
         import torch
         from .ops import TokenLogprobs, token_logprobs
         cache = self._refs[1]
@@ -250,13 +257,16 @@ class Engine:
         most = max(1, min(n, SCORE_BYTES // (4 * self.B * V)))
         logits = torch.empty(most, self.B, V, dtype=torch.float32, device=dev)
         out = torch.empty(most, self.B, dtype=torch.int32, device=dev)
+        none = token_logprobs(logits[:0], tokens[:0], top_k)   # (refuses a bad top_k)
+        if n == 0:
+            return none
+        if n > self.room():
+            raise XlpkError(_abi.XLPK_ERR_KV_FULL, "Engine.score", detail=f"{n} tokens, room for {self.room()}")
         parts = []
         for s in range(0, n, most):
             t = tokens[s:s + most]
             self.decode(t.shape[0], out, forced=t, logits=logits)
             parts.append(token_logprobs(logits[:t.shape[0]], t, top_k))
-        if not parts:
-            return token_logprobs(logits[:0], tokens, top_k)
         return TokenLogprobs(*(torch.cat(f) if f[0] is not None else None for f in zip(*parts)))
 
     def page_pool(self, seq_lens, refs=None):

@@ -115,3 +115,8 @@ def test_struct_layout_matches_header(tmp_path):
 
 def test_debug_logits_rejects_a_null_handle(lib):
     assert lib.xlpk_debug_logits(None, None, None) == _abi.XLPK_ERR_INVALID_ARG
+
+
+def test_get_room_rejects_a_null_handle(lib):
+    n = C.c_int32(-1)
+    assert lib.xlpk_get_room(None, C.byref(n)) == _abi.XLPK_ERR_INVALID_ARG and n.value == -1

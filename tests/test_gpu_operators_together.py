@@ -98,6 +98,31 @@ def test_score_in_parts_is_the_same(cuda_device, monkeypatch):
     assert all(torch.equal(a, b) for a, b in zip(*whole))
 
 
+def test_a_refused_score_moves_nothing(cuda_device, monkeypatch):
+    import persistent_decode_b200.engine as eng
+    from persistent_decode_b200 import XlpkError, _abi
+    cfg = synth.get_config("tiny", batch=2, steps=9)
+    m = workload.build(cfg, device=cuda_device)
+    monkeypatch.setattr(eng, "SCORE_BYTES", 1 << 17)       # four steps at a time
+    workload.reset_state(m)
+    room = m.engine.max_seq - cfg.kv_len
+    assert m.engine.room() == room
+    g = torch.Generator().manual_seed(5)
+    toks = torch.randint(0, cfg.vocab, (room + 1, 2), dtype=torch.int32, generator=g).to(cuda_device)
+    want = m.engine.score(toks[:room], top_k=2)
+    assert m.engine.room() == 0
+    workload.reset_state(m)
+    for n, k, status in ((room + 1, 2, _abi.XLPK_ERR_KV_FULL), (5, 65, _abi.XLPK_ERR_UNSUPPORTED), (5, -1, _abi.XLPK_ERR_INVALID_ARG),
+                         (5, cfg.vocab + 1, _abi.XLPK_ERR_INVALID_ARG)):
+        with pytest.raises(XlpkError) as e:
+            m.engine.score(toks[:n], top_k=k)
+        assert e.value.status == status
+        assert m.engine.room() == room
+    # positions and pending tokens are what they were: the same scores come out
+    assert all(torch.equal(a, b) for a, b in zip(m.engine.score(toks[:room], top_k=2), want))
+    m.engine.check()
+
+
 def test_attention_reads_the_engines_cache(cuda_device):
     # the paged and the contiguous cache of the same model, bf16 and e4m3, after a decode
     for kv8 in (False, True):
