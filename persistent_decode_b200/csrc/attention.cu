@@ -154,7 +154,7 @@ struct Shape {
   static constexpr int PT = IO32 && !KV8 ? 3 : 2;       // terms of p
   static constexpr int QR = D / 8;                      // registers of one term of one row
   static constexpr bool LOW = WIDE && QT > 1;           // the lower terms' scores have sums of their own (else: rows 8-15)
-  static constexpr int SHIFT = KV8 ? 10 : 0;            // p is held times 2^SHIFT
+  static constexpr float SHIFT = KV8 ? 10.f : 0.f;      // p is held times 2^SHIFT: fp16 has 2^-14 for its lower term then
   static constexpr int SLOT = ROWS * (D + 2);           // floats of a partial result
 };
 
@@ -276,7 +276,7 @@ __device__ inline float ex2(float x) {
   return r;
 }
 
-__device__ inline float lse_of(float m, float l, int shift) { return l == 0 ? -INFINITY : (m - shift) * kLn2 + logf(l); }
+__device__ inline float lse_of(float m, float l) { return l == 0 ? -INFINITY : m * kLn2 + logf(l); }
 
 template <class S>
 __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_constant__ Args args) {
@@ -663,7 +663,9 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         for (int nt = 1; nt < 4; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        top = fmaxf(top * rs[r], m[r]);
+        // The running "maximum" is what exponents are measured from: the maximum less SHIFT, rounded, and the
+        // same number for p, for what is rescaled and for the joins, so that its rounding cancels.
+        top = fmaxf(fmaf(top, rs[r], -S::SHIFT), m[r]);
         const float base = top == -INFINITY ? 0.f : top;
         fall[r] = ex2(m[r] - base);
         grow = grow || top != m[r];
@@ -671,8 +673,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         float sum = 0.f;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          // (the exponent is rounded once, near 0 where it counts)
-          float p0 = ex2(fmaf(s[nt][2 * r], rs[r], S::SHIFT - base)), p1 = ex2(fmaf(s[nt][2 * r + 1], rs[r], S::SHIFT - base));
+          // (the exponent is rounded once, near SHIFT where it counts)
+          float p0 = ex2(fmaf(s[nt][2 * r], rs[r], -base)), p1 = ex2(fmaf(s[nt][2 * r + 1], rs[r], -base));
           sum += p0 + p1;
 #pragma unroll
           for (int k = 0; k < S::PT; ++k) pt[r][k][nt] = term<S::KV8>(p0, p1);
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         store_out<S::IO32>(a.out_dev, w.b * a.out_seq_stride + (w.h * group + head) * a.out_head_stride + d,
                            make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
         if (d == 0 && a.lse_dev)
-          a.lse_dev[static_cast<long long>(w.b) * a.n_q_heads + w.h * group + head] = lse_of(top, den, S::SHIFT);
+          a.lse_dev[static_cast<long long>(w.b) * a.n_q_heads + w.h * group + head] = lse_of(top, den);
       } else {
         *reinterpret_cast<float4*>(slot + head * D + d) = sum;
         if (d == 0) slot[S::ROWS * D + head] = top, slot[S::ROWS * (D + 1) + head] = den;
@@ -832,7 +834,7 @@ __device__ inline void store_joined(const xlpk_attention_args& a, const int4& j,
   const int h = j.y * (a.n_q_heads / a.n_kv_heads) + head;
   store_out<S::IO32>(a.out_dev, j.x * a.out_seq_stride + h * a.out_head_stride + d,
                      make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
-  if (d == 0 && a.lse_dev) a.lse_dev[static_cast<long long>(j.x) * a.n_q_heads + h] = lse_of(top, den, S::SHIFT);
+  if (d == 0 && a.lse_dev) a.lse_dev[static_cast<long long>(j.x) * a.n_q_heads + h] = lse_of(top, den);
 }
 
 // The pieces of every segment that one worker begins and another ends, joined by their maxima:

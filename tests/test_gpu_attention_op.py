@@ -193,6 +193,34 @@ def test_peaked_scores_and_scale(cuda_device):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [40, 1500])
+def test_positions_of_different_tiles_weigh_by_the_same_measure(cuda_device, B, kv):
+    """Two positions of five tiles carry all of the weight, the later one more of it; the ratio of their
+    outputs is 2^(x0 - x1) whatever the softmax is measured from.  Scores are exact: one product with 1, of q
+    whose 23 bits two fp16 terms hold, times a scale of which scale * log2(e) is 1 in fp32 (it is 2.8e-9
+    off ln 2, which adds 8 x 2.8e-9).  So the ratio carries three exponentials (2^-22 each: both weights and
+    the rescaling of the first), the split of both weights (two 11-bit terms: 2^-24 each), a rescaling and
+    two products of the result (2^-24 each): 17 x 2^-24 and that, below 18 x 2^-24."""
+    H, D, n = 8, 64, 80
+    g = torch.Generator().manual_seed(31)
+    x = -8 + torch.randint(1, 1 << 21, (B, H, 2), generator=g).double() * 2.0 ** -20
+    x = x.sort(dim=2).values
+    q = torch.zeros(B, H, D)
+    q[..., :2], q[..., 2] = x.float(), -256.0
+    assert torch.equal(q[..., :2].double(), x)
+    k, v = torch.zeros(B, 1, n, D), torch.zeros(B, 1, n, D)
+    k[:, :, :, 2] = 1
+    for i, t in enumerate((5, n - 1)):
+        k[:, :, t, 2], k[:, :, t, i], v[:, :, t, i] = 0, 1, 1
+    k, v = ((t.to(E4M3).view(torch.uint8) if kv == "e4m3" else t.to(torch.bfloat16)).cuda() for t in (k, v))
+    out = decode_attention(q.cuda(), k, v, torch.full((B,), n, dtype=torch.int32, device=cuda_device),
+                           scale=float(torch.tensor(math.log(2)))).double().cpu()
+    ratio = out[..., 0] / out[..., 1]
+    want = torch.exp2(x[..., 0] - x[..., 1])
+    assert float((ratio / want - 1).abs().max()) <= 18 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("H,KH,D,page", [(8, 2, 64, 16), (8, 2, 128, 0), (5, 5, 128, 24), (16, 1, 64, 5)])
 def test_stores_the_new_row(cuda_device, H, KH, D, page, io, kv):
