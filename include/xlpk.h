@@ -461,7 +461,8 @@ xlpk_status xlpk_tc_gemm_tile(const void* w_dev, int32_t n, int32_t k, const flo
  *    (else XLPK_ERR_INVALID_ARG; lse_dev, seq_lens_dev, page_table_dev and
  *    status_dev: of 4).
  *  - n = 0: the output row is zero, lse -inf, nothing is stored.
- *  - q and the visible entries are finite; what stands elsewhere may be anything.
+ *  - q and the visible entries are finite, and so, in fp32, are the scores (for a bf16
+ *    cache q.k before it is scaled too); what stands elsewhere may be anything.
  *  - Capacities (table_cols * page_size) below 2^31 - 64 positions, and below about
  *    2^35 over all sequences and kv heads (else XLPK_ERR_UNSUPPORTED).
  *  - Rows of the cache that no sequence sees are not read: pages a window has
@@ -495,7 +496,7 @@ typedef struct xlpk_attention_args {
   int32_t n_pages, page_size, table_cols;
   int32_t io_dtype, kv_dtype;      /* kv_dtype: XLPK_DTYPE_BF16 or XLPK_DTYPE_FP8_E4M3 */
   int32_t window, sinks;           /* 0 window: every position is visible */
-  float scale;                     /* finite, > 0 */
+  float scale;                     /* > 0, below 2^127 */
   float k_scale, v_scale;          /* e4m3 cache: powers of two in [2^-24, 2^24]; else ignored */
 } xlpk_attention_args;
 

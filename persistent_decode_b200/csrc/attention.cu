@@ -52,7 +52,6 @@ using namespace xlpk;
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinWarps = 8;
 constexpr int kThreads = kJoinWarps * 32;   // of the join
@@ -64,6 +63,8 @@ struct Args {
   xlpk_attention_args a;
   float* parts;     // [workers][2] slots of partial results
   int ctas;         // of the attention
+  float s2;         // scale * log2(e); for an e4m3 cache s2 * 2^exp is that times k_scale, s2 in [0.5, 1]
+  int exp;
   int page_shift;   // log2 of page_size, or -1
   bool flat;        // the visible rows of a tile are in one page
   int4* joins;      // [workers] (sequence, kv head, last worker, -) of the segment that a worker begins and another ends; .x < 0: none
@@ -268,6 +269,9 @@ __device__ inline void copy_async(uint32_t dst, const void* src, bool real) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(real ? 8 : 0) : "memory");
 }
+
+// -126 <= e <= 127
+__device__ inline float power_of_2(int e) { return __int_as_float((e + 127) << 23); }
 
 // 2^x to 2^-22, 0 for -inf.
 __device__ inline float ex2(float x) {
@@ -533,13 +537,12 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
     if (team == 1) __syncwarp();
     else __syncthreads();
   };
-  const float s2 = a.scale * kLog2e * (S::KV8 ? a.k_scale : 1.f);
   int x = x0;   // the segment's first tile here
   int stage = 0;
   for (;;) {
     // ---- q of the segment's heads, as terms
     uint32_t q[S::WIDE ? 2 : 1][S::QT][S::QR];
-    float rs[S::WIDE ? 2 : 1];
+    float rs[S::WIDE ? 2 : 1];   // what makes powers of 2 of the row's scores (e4m3; else args.s2 does)
 #pragma unroll
     for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
       float v[D / 4];
@@ -554,20 +557,21 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) v[i] = 0.f;
       }
-      rs[r] = s2;
       if (S::KV8) {
         // fp16 terms: the row is scaled by the power of two that brings its largest entry to
-        // [2^10, 2^11), where 11 bits of it, and what they leave, are held far below 2^-24 of it
+        // [2^10, 2^11), where 11 bits of it, and what they leave, are held far below 2^-24 of it.
+        // (2^e alone may be out of range, and so may the scale's product with 2^-e before it is whole.)
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const int e = top > 0x1p-100f && top < 0x1p100f ? 10 - ilogbf(top) : 0;
-        const float up = ldexpf(1.f, e);
-        rs[r] *= ldexpf(1.f, -e);
+        const int e = top > 0.f && top < INFINITY ? 10 - ilogbf(top) : 0;
+        const float up = power_of_2(min(e, 100)), more_up = power_of_2(max(e - 100, 0));
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) v[i] *= up;
+        for (int i = 0; i < D / 4; ++i) v[i] *= up, v[i] *= more_up;
+        const int down = min(max(args.exp - e, -252), 252), half = down / 2;
+        rs[r] = fminf(args.s2 * power_of_2(half) * power_of_2(down - half), 0x1.fffffep127f);   // (finite: scores of 0 stay 0)
       }
 #pragma unroll
       for (int i = 0; i < S::QR; ++i)
@@ -665,7 +669,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         // The running "maximum" is what exponents are measured from: the maximum less SHIFT, rounded, and the
         // same number for p, for what is rescaled and for the joins, so that its rounding cancels.
-        top = fmaxf(fmaf(top, rs[r], -S::SHIFT), m[r]);
+        const float mult = S::KV8 ? rs[r] : args.s2;
+        top = fmaxf(fmaf(top, mult, -S::SHIFT), m[r]);
         const float base = top == -INFINITY ? 0.f : top;
         fall[r] = ex2(m[r] - base);
         grow = grow || top != m[r];
@@ -674,7 +679,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           // (the exponent is rounded once, near SHIFT where it counts)
-          float p0 = ex2(fmaf(s[nt][2 * r], rs[r], -base)), p1 = ex2(fmaf(s[nt][2 * r + 1], rs[r], -base));
+          float p0 = ex2(fmaf(s[nt][2 * r], mult, -base)), p1 = ex2(fmaf(s[nt][2 * r + 1], mult, -base));
           sum += p0 + p1;
 #pragma unroll
           for (int k = 0; k < S::PT; ++k) pt[r][k][nt] = term<S::KV8>(p0, p1);
@@ -920,8 +925,8 @@ xlpk_status check_args(const xlpk_attention_args* a) {
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: a negative count");
   if (static_cast<int64_t>(a->table_cols) * a->page_size > INT32_MAX - 4 * kTile)
     return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: a capacity of 2^31 - 64 positions or more");
-  if (!(a->scale > 0) || !std::isfinite(a->scale))
-    return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: scale is not finite and positive");
+  if (!(a->scale > 0) || !(a->scale < 0x1p127f))
+    return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: scale is not positive and below 2^127");
   if (a->kv_dtype == XLPK_DTYPE_FP8_E4M3 && (!power_of_two_scale(a->k_scale) || !power_of_two_scale(a->v_scale)))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: cache scales are powers of two in [2^-24, 2^24]");
   if (static_cast<int64_t>(a->n_seqs) * a->n_kv_heads >
@@ -1004,6 +1009,9 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   if (a->n_seqs == 0) return XLPK_OK;
   Args args;
   args.a = *a;
+  const double s2 = static_cast<double>(a->scale) * 1.4426950408889634074;
+  args.exp = 0;
+  args.s2 = static_cast<float>(a->kv_dtype == XLPK_DTYPE_FP8_E4M3 ? std::frexp(s2 * a->k_scale, &args.exp) : s2);
   args.page_shift = (a->page_size & (a->page_size - 1)) == 0 ? __builtin_ctz(a->page_size) : -1;
   args.flat = a->page_size % kTile == 0 || a->table_cols == 1;   // (behind its only page no position is visible)
   args.ctas = std::min(sms, kMaxCtas);

@@ -220,6 +220,18 @@ def test_positions_of_different_tiles_weigh_by_the_same_measure(cuda_device, B, 
     assert float((ratio / want - 1).abs().max()) <= 18 * 2.0 ** -24
 
 
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("power", [124, 101, 99, -99, -101, -117, -129])
+def test_queries_of_any_size_over_e4m3(cuda_device, power, H, KH, D, io):
+    # q near either end of fp32's range, with a scale that makes ordinary scores of it
+    s = make(4, [1, 40, 333, 16], H, KH, D, 16, "e4m3", io, seed=power + 200)
+    s["q"] = (s["q"].double() * 2.0 ** power).to(io)
+    assert bool(s["q"].isfinite().all()) and float(s["q"].abs().max()) > 0
+    scale = 2.0 ** (-power - 3)
+    check(s, *call(s, scale=scale), scale=scale)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("H,KH,D,page", [(8, 2, 64, 16), (8, 2, 128, 0), (5, 5, 128, 24), (16, 1, 64, 5)])

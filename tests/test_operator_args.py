@@ -59,6 +59,12 @@ def test_attention_refuses_unsupported(lib, bad):
     assert lib.xlpk_decode_attention(C.byref(a), P, 1 << 30, None) == UNSUPPORTED
 
 
+def test_attention_refuses_a_scale_that_overflows(lib):
+    for scale in (2.0 ** 127, 3e38):     # times log2(e) it has no place in fp32
+        assert lib.xlpk_decode_attention(C.byref(_attn(scale=scale)), P, 1 << 30, None) == INVALID
+        assert b"scale" in lib.xlpk_last_cuda_error()
+
+
 def test_attention_workspace(lib):
     a = _attn()
     n = lib.xlpk_decode_attention_workspace(C.byref(a))
