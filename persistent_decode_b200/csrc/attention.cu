@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) v[i] *= up, v[i] *= more_up;
         const int down = min(max(args.exp - e, -252), 252), half = down / 2;
-        rs[r] = fminf(args.s2 * power_of_2(half) * power_of_2(down - half), 0x1.fffffep127f);   // (finite: scores of 0 stay 0)
+        // (neither infinity nor 0: scores of 0 stay 0, those of hidden positions -inf)
+        rs[r] = fmaxf(fminf(args.s2 * power_of_2(half) * power_of_2(down - half), 0x1.fffffep127f), 0x1p-126f);
       }
 #pragma unroll
       for (int i = 0; i < S::QR; ++i)

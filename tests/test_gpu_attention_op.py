@@ -233,6 +233,16 @@ def test_queries_of_any_size_over_e4m3(cuda_device, power, H, KH, D, io):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("size,scale", [(2.0 ** -100, 2.0 ** -100), (2.0 ** -120, 2.0 ** -149), (0.0, 2.0 ** 126), (1.0, 2.0 ** -149)])
+def test_scores_that_vanish(cuda_device, size, scale, H, KH, D, kv):
+    # scores of (next to) nothing, in rows whose last tile has hidden positions: every visible one weighs the same
+    s = make(4, [1, 40, 333, 17], H, KH, D, 16, kv, torch.float32, seed=41)
+    s["q"] = (s["q"].double() * size).float()
+    check(s, *call(s, scale=scale, window=100, sinks=3), scale=scale, window=100, sinks=3)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("H,KH,D,page", [(8, 2, 64, 16), (8, 2, 128, 0), (5, 5, 128, 24), (16, 1, 64, 5)])
 def test_stores_the_new_row(cuda_device, H, KH, D, page, io, kv):
