@@ -53,6 +53,7 @@ using namespace xlpk;
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFarScore = 0x1p22f;   // in powers of 2: fp32's step is half of one
 constexpr int kJoinWarps = 8;
 constexpr int kThreads = kJoinWarps * 32;   // of the join
 constexpr int kMaxCtas = 160;               // one for each SM
@@ -670,8 +671,17 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
         // The running "maximum" is what exponents are measured from: the maximum less SHIFT, rounded, and the
         // same number for p, for what is rescaled and for the joins, so that its rounding cancels.
-        const float mult = S::KV8 ? rs[r] : args.s2;
-        top = fmaxf(fmaf(top, mult, -S::SHIFT), m[r]);
+        float mult = S::KV8 ? rs[r] : args.s2;
+        if (fabsf(top * mult) >= kFarScore) {
+          // Out here a rounded maximum is far from the product that it is rounded from (2^27: 8, which fp16
+          // does not stand): scores are rounded first, as coarsely, and the largest has exponent 0.
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) s[nt][2 * r] *= mult, s[nt][2 * r + 1] *= mult;
+          top = fmaxf(top * mult, m[r]);
+          mult = 1.f;
+        } else {
+          top = fmaxf(fmaf(top, mult, -S::SHIFT), m[r]);
+        }
         const float base = top == -INFINITY ? 0.f : top;
         fall[r] = ex2(m[r] - base);
         grow = grow || top != m[r];

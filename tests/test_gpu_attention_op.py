@@ -233,6 +233,41 @@ def test_queries_of_any_size_over_e4m3(cuda_device, power, H, KH, D, io):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("power", [12, 21, 23, 25, 27, 29, 31, 33, 50, 90])
+def test_scores_of_any_finite_size(cuda_device, power, H, KH, D, io, kv):
+    # The score of position t is 2^power x_t with whole x_t in -8 .. 8, but for one of 9: at these distances
+    # (2^12 and more) it has all of the weight, whatever its sign and wherever it stands, and the output is
+    # its v: to half a step of the output's type, and in fp32 what p's split (2^-24), the sums of its products
+    # (2^-23 each of two), the sum of the terms, the quotient and the product (2^-24 each) add: 2^-21
+    lens = [1, 40, 333, 700]
+    s = make(len(lens), lens, H, KH, D, 0, kv, io, seed=power)
+    g = torch.Generator().manual_seed(power)
+    for sign in (1, -1):
+        x = torch.randint(-8, 9, (len(lens), KH, s["P"]), generator=g)
+        best = [int(torch.randint(0, n, (1,), generator=g)) for n in lens]
+        if sign < 0:
+            x = x.abs() - 30           # -30 .. -22
+        for b, t in enumerate(best):
+            x[b, :, t] = 9 if sign > 0 else -20
+        k = torch.zeros(len(lens), KH, s["P"], D)
+        k[..., 0], k[..., 1] = (x // 4).float(), (x % 4).float()       # x = 4 k0 + k1: exact in either type
+        s["k"] = (k.to(E4M3).view(torch.uint8) if kv == "e4m3" else k.to(torch.bfloat16)).cuda()
+        s["q"] = torch.zeros(len(lens), H, D, dtype=io, device=cuda_device)
+        s["q"][..., 0], s["q"][..., 1] = 2.0 ** (power + 2), 2.0 ** power
+        out, lse = decode_attention(s["q"], s["k"], s["v"], s["lens"], scale=1.0, v_scale=s["scale_kv"], return_lse=True)
+        v = values(s["v"], s["scale_kv"]).cpu()
+        want = torch.stack([v[b, :, t] for b, t in enumerate(best)]).repeat_interleave(H // KH, 1)
+        slack = torch.finfo(io).eps / 2 + 2.0 ** -21
+        assert bool(((out.double().cpu() - want).abs() <= slack * want.abs()).all())
+        score = 2.0 ** power * (9 if sign > 0 else -20)
+        # log2(e), its product with the score, ln 2, the product with that and the sum: five roundings; the
+        # log of the weights' sum, of 1 or 2^10: two
+        assert float((lse.double() - score).abs().max()) <= 5 * 2.0 ** -24 * abs(score) + 2 * 2.0 ** -24 * 10
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
 @pytest.mark.parametrize("size,scale", [(2.0 ** -100, 2.0 ** -100), (2.0 ** -120, 2.0 ** -149), (0.0, 2.0 ** 126), (1.0, 2.0 ** -149)])
 def test_scores_that_vanish(cuda_device, size, scale, H, KH, D, kv):
