@@ -527,7 +527,7 @@ typedef struct xlpk_page_pool {
   int32_t* status_dev;             /* one word */
   int32_t n_layers, n_pages, n_kv_heads, page_size;
   int32_t row_bytes;               /* bytes of one position of one kv head, a multiple of 16 */
-  int32_t rows, cols;              /* rows <= 1024 */
+  int32_t rows, cols;              /* rows <= 1024; n_pages, cols <= 2^30 (else XLPK_ERR_UNSUPPORTED) */
 } xlpk_page_pool;
 
 /* Bytes of the workspace of xlpk_pages_fork and xlpk_pages_compact (16-byte aligned). */

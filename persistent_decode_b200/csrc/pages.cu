@@ -389,6 +389,8 @@ xlpk_status check_pool(const xlpk_page_pool* p) {
       p->row_bytes < 16 || p->row_bytes % 16)
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_pages: a size is not positive, or row_bytes not a multiple of 16");
   if (p->rows > kMaxRows) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_pages: more than 1024 rows");
+  // (indexes run past their end by up to a CTA's threads)
+  if (p->n_pages > 1 << 30 || p->cols > 1 << 30) return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_pages: more than 2^30 pages or columns");
   if (static_cast<int64_t>(p->cols) * p->page_size > INT32_MAX)
     return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_pages: a table row of 2^31 positions or more");
   if (!p->k_dev || !p->v_dev || !p->page_table_dev || !p->seq_lens_dev || !p->refs_dev || !p->status_dev)

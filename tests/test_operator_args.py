@@ -112,6 +112,14 @@ def test_pages_refuse_large_tables(lib):
             assert call() == UNSUPPORTED, name
 
 
+def test_pages_refuse_counts_near_2_31(lib):
+    # loops over pages and columns step 1024 at a time, in 32 bits
+    for big in (dict(n_pages=(1 << 30) + 1), dict(n_pages=(1 << 31) - 1), dict(cols=(1 << 30) + 1, page_size=1),
+                dict(cols=(1 << 31) - 1, page_size=1)):
+        for name, call in _page_calls(lib, _pool(**big), size=1 << 40).items():
+            assert call() == UNSUPPORTED, (name, big)
+
+
 def test_pages_refuse_bad_arguments(lib):
     p = _pool()
     n = lib.xlpk_pages_workspace(C.byref(p))
