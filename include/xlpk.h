@@ -447,7 +447,7 @@ xlpk_status xlpk_tc_gemm_tile(const void* w_dev, int32_t n, int32_t k, const flo
  * t >= n - window, or t < sinks).  With k_new / v_new the call first stores them,
  * rounded as a decode rounds (bf16, or the e4m3 code of x / scale, to nearest even,
  * saturated), as the row of position n - 1, and attends over what it stored.
- *  - head_dim 64 or 128; any n_q_heads / n_kv_heads up to 16; q, k_new, v_new and
+ *  - head_dim 64 or 128; n_q_heads up to 2^20, n_q_heads / n_kv_heads up to 16; q, k_new, v_new and
  *    out are all io_dtype: XLPK_DTYPE_BF16 or XLPK_DTYPE_FP32.  Sums, softmax
  *    statistics and lse are fp32.
  *  - The cache is the one of xlpk_kv for one layer, in any order whose rows of

@@ -929,6 +929,8 @@ xlpk_status check_args(const xlpk_attention_args* a) {
   if (!shape_ok(a)) return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: n_seqs, heads or head_dim");
   if ((a->head_dim != 64 && a->head_dim != 128) || a->n_q_heads / a->n_kv_heads > 16)
     return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: head_dim 64 or 128, at most 16 query heads per kv head");
+  if (a->n_q_heads > 1 << 20)   // (a row of them is counted in 32 bits)
+    return refuse(XLPK_ERR_UNSUPPORTED, "xlpk_decode_attention: more than 2^20 query heads");
   if ((a->io_dtype != XLPK_DTYPE_BF16 && a->io_dtype != XLPK_DTYPE_FP32) ||
       (a->kv_dtype != XLPK_DTYPE_BF16 && a->kv_dtype != XLPK_DTYPE_FP8_E4M3))
     return refuse(XLPK_ERR_INVALID_ARG, "xlpk_decode_attention: io_dtype is bf16 or fp32, kv_dtype bf16 or e4m3");

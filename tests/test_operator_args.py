@@ -59,6 +59,13 @@ def test_attention_refuses_unsupported(lib, bad):
     assert lib.xlpk_decode_attention(C.byref(a), P, 1 << 30, None) == UNSUPPORTED
 
 
+def test_attention_refuses_heads_past_32_bits(lib):
+    # n_q_heads * head_dim is counted in 32 bits where a sequence without positions is written
+    a = _attn(n_seqs=1, n_q_heads=1 << 25, n_kv_heads=1 << 25, table_cols=1)
+    assert lib.xlpk_decode_attention(C.byref(a), P, 1 << 30, None) == UNSUPPORTED
+    assert b"heads" in lib.xlpk_last_cuda_error()
+
+
 def test_attention_refuses_a_scale_that_overflows(lib):
     for scale in (2.0 ** 127, 3e38):     # times log2(e) it has no place in fp32
         assert lib.xlpk_decode_attention(C.byref(_attn(scale=scale)), P, 1 << 30, None) == INVALID
