@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes as C
 import struct
+from operator import index
 from typing import NamedTuple, Optional
 
 import torch
@@ -57,9 +58,13 @@ def _tensor(t, name: str, dim: int, dtypes, device: int) -> None:
 
 
 def _int32(v, name: str) -> int:
-    if not -(1 << 31) <= v < 1 << 31:
-        _refuse(f"{name} = {v} does not fit an int32")
-    return int(v)
+    try:
+        n = index(v)
+    except TypeError:
+        _refuse(f"{name} = {v!r} is not an integer")
+    if not -(1 << 31) <= n < 1 << 31:
+        _refuse(f"{name} = {n} does not fit an int32")
+    return n
 
 
 def _distinct(t) -> bool:

@@ -191,3 +191,13 @@ def test_python_refuses_what_is_not_on_a_gpu():
     with pytest.raises(ValueError):
         PagePool(torch.zeros(1, 4, 2, 8, 64), torch.zeros(1, 4, 2, 8, 64), torch.zeros(1, 4, dtype=torch.int32),
                  torch.zeros(1, dtype=torch.int32))
+
+
+def test_integers_are_not_rounded():
+    # a window, an alternative count or a page of 2.5 is refused, not taken for 2
+    from persistent_decode_b200.ops import _int32
+    import numpy as np
+    assert [_int32(v, "x") for v in (3, -1, True, np.int64(7), torch.tensor(5))] == [3, -1, 1, 7, 5]
+    for bad in (2.5, 2.0, float("nan"), "3", None, torch.tensor(2.0), 1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError):
+            _int32(bad, "x")
