@@ -408,7 +408,8 @@ xlpk_status xlpk_get_info(xlpk_handle h, xlpk_info* out);
 /* Human-readable name of a status; "XLPK_ERR_UNKNOWN" for other values. */
 const char* xlpk_status_string(int32_t status);
 
-/* Text of the last CUDA error seen by this thread's calls ("" if none). */
+/* Text of the last CUDA error seen by this thread's calls, or why one of the
+ * stand-alone operators was refused since ("" if none). */
 const char* xlpk_last_cuda_error(void);
 
 /* One batch-8 projection on the tcgen05 tensor cores:

@@ -35,6 +35,9 @@ class XlpkError(RuntimeError):
         msg = lib.xlpk_status_string(status).decode()
         if detail is None:
             detail = lib.xlpk_last_cuda_error().decode()
+            about = detail.split(":")[0]
+            if about.startswith("xlpk_") and not what.startswith(about):
+                detail = ""     # why an earlier call of another function was refused
         super().__init__(f"{what}: {msg}" + (f" ({detail})" if detail else ""))
         self.status = status
 

@@ -201,3 +201,13 @@ def test_integers_are_not_rounded():
     for bad in (2.5, 2.0, float("nan"), "3", None, torch.tensor(2.0), 1 << 31, -(1 << 31) - 1):
         with pytest.raises(ValueError):
             _int32(bad, "x")
+
+
+def test_an_error_does_not_quote_another_calls_refusal(lib):
+    from persistent_decode_b200 import XlpkError
+    assert lib.xlpk_token_logprobs(P, _abi.XLPK_DTYPE_FP32, 1, 100, 100, P, 65, P, None, None, P, P, None) == UNSUPPORTED
+    assert "top_k over 64" in str(XlpkError(UNSUPPORTED, "xlpk_token_logprobs"))
+    assert str(XlpkError(_abi.XLPK_ERR_KV_FULL, "xlpk_decode")) == "xlpk_decode: XLPK_ERR_KV_FULL"
+    assert _page_calls(lib, _pool(rows=1025))["fork"]() == UNSUPPORTED
+    assert "1024 rows" in str(XlpkError(UNSUPPORTED, "xlpk_pages_fork"))      # (its text begins "xlpk_pages:")
+    assert "1024 rows" not in str(XlpkError(INVALID, "xlpk_create"))
