@@ -193,22 +193,24 @@ def test_peaked_scores_and_scale(cuda_device):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-@pytest.mark.parametrize("B", [40, 1500])
-def test_positions_of_different_tiles_weigh_by_the_same_measure(cuda_device, B, kv):
+@pytest.mark.parametrize("B,H,KH,D", [(40, 8, 1, 64), (1500, 8, 1, 64), (300, 8, 2, 128), (40, 16, 1, 64), (300, 16, 1, 128),
+                                      (200, 9, 1, 128), (300, 3, 3, 128)])
+def test_positions_of_different_tiles_weigh_by_the_same_measure(cuda_device, B, H, KH, D, kv):
     """Two positions of five tiles carry all of the weight, the later one more of it; the ratio of their
     outputs is 2^(x0 - x1) whatever the softmax is measured from.  Scores are exact: one product with 1, of q
     whose 23 bits two fp16 terms hold, times a scale of which scale * log2(e) is 1 in fp32 (it is 2.8e-9
     off ln 2, which adds 8 x 2.8e-9).  So the ratio carries three exponentials (2^-22 each: both weights and
     the rescaling of the first), the split of both weights (two 11-bit terms: 2^-24 each), a rescaling and
-    two products of the result (2^-24 each): 17 x 2^-24 and that, below 18 x 2^-24."""
-    H, D, n = 8, 64, 80
+    two products of the result (2^-24 each): 17 x 2^-24 and that, below 18 x 2^-24 (sums of the terms are exact).
+    A term of q or p that is lost shows: the third of bf16 q leaves up to 2^-18 of 8, that of p 2^-18."""
+    n = 80
     g = torch.Generator().manual_seed(31)
     x = -8 + torch.randint(1, 1 << 21, (B, H, 2), generator=g).double() * 2.0 ** -20
     x = x.sort(dim=2).values
     q = torch.zeros(B, H, D)
     q[..., :2], q[..., 2] = x.float(), -256.0
     assert torch.equal(q[..., :2].double(), x)
-    k, v = torch.zeros(B, 1, n, D), torch.zeros(B, 1, n, D)
+    k, v = torch.zeros(B, KH, n, D), torch.zeros(B, KH, n, D)
     k[:, :, :, 2] = 1
     for i, t in enumerate((5, n - 1)):
         k[:, :, t, 2], k[:, :, t, i], v[:, :, t, i] = 0, 1, 1

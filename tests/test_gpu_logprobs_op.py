@@ -166,6 +166,37 @@ def test_masks_of_finite_values(cuda_device, low, dtype):
     check(x, tok, run(x, tok, 64), 64)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("V,std", [(7, 1.0), (100, 0.1), (1023, 3.0), (4096, 0.5), (4096, 8.0)])
+def test_digits_of_short_rows(cuda_device, V, std, dtype):
+    """Bounds by the additions that rows this short take.  Of w = e^(x-m) = 2^y: the exponential 2^-22, the
+    rounding of y and of log2(e) 2^-23 |y| together, of which the weighted mean is log2(V) at most; of a sum
+    of V terms over 256 threads: V/256 + 16 in a thread, 5 and 16 across threads and warps, 2^-24 each; the
+    factor that moves it to m: 2^-22.  So r = 2^-21 + 2^-23 log2(V) + (V/256 + 37) 2^-24 for the others' sum s.
+    log1p passes on r s / (1+s) and adds its own 2^-23, x - m and the difference 2^-24 each of |logprob| or less:
+    r s / (1+s) + 2^-22 |logprob|.  The mean of |x - m|, M, carries r twice (numerator, denominator) and 2^-23."""
+    g = torch.Generator().manual_seed(V)
+    R = 64
+    x = (torch.randn(R, V, generator=g) * std).to(dtype)
+    tok = torch.randint(0, V, (R,), generator=g)
+    k = min(V, 64)
+    got = run(x, tok.tolist(), k)
+    xd = x.double()
+    lp = torch.log_softmax(xd, 1)
+    p = lp.exp()
+    s = p.amax(1).reciprocal() - 1
+    M = (p * (xd.amax(1, keepdim=True) - xd)).sum(1)
+    r = 2.0 ** -21 + 2.0 ** -23 * math.log2(V) + (V / 256 + 37) * 2.0 ** -24
+    slack = r * s / (1 + s)
+    want = lp.gather(1, tok[:, None])[:, 0]
+    assert bool(((got.logprob.double() - want).abs() <= slack + 2.0 ** -22 * want.abs()).all())
+    want = lp.gather(1, got.top_ids.long())
+    assert bool(((got.top_logprobs.double() - want).abs() <= slack[:, None] + 2.0 ** -22 * want.abs()).all())
+    want = -(p * lp).sum(1)
+    bound = slack + 2.0 ** -22 * torch.log1p(s) + (2 * r + 2.0 ** -23) * M + 2.0 ** -24 * want
+    assert bool(((got.entropy.double() - want).abs() <= bound).all())
+
+
 def test_a_certain_token_keeps_its_small_logprob(cuda_device):
     # log p of the best token is -s with s = 9 e^-20: far below the step of 1, kept to relative 2^-13
     x = torch.zeros(1, 10)
