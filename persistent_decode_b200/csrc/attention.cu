@@ -1022,6 +1022,8 @@ extern "C" xlpk_status xlpk_decode_attention(const xlpk_attention_args* a, void*
   if (a->n_seqs == 0) return XLPK_OK;
   Args args;
   args.a = *a;
+  // (copies of rows that are not there read nothing, but name the pool's start: with no pages, some memory)
+  if (a->n_pages == 0) args.a.k_dev = args.a.v_dev = workspace_dev;
   const double s2 = static_cast<double>(a->scale) * 1.4426950408889634074;
   args.exp = 0;
   args.s2 = static_cast<float>(a->kv_dtype == XLPK_DTYPE_FP8_E4M3 ? std::frexp(s2 * a->k_scale, &args.exp) : s2);

@@ -414,6 +414,21 @@ def test_no_sequences(cuda_device):
     assert got.shape == (0, 4, 64)
 
 
+@pytest.mark.parametrize("kv", [torch.bfloat16, torch.uint8], ids=["bf16", "e4m3"])
+def test_a_pool_without_pages(cuda_device, kv):
+    none = torch.empty((0, 2, 16, 64), dtype=kv, device=cuda_device)
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device=cuda_device)
+    table = torch.zeros((3, 2), dtype=torch.int32, device=cuda_device)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    lens = torch.tensor([0, 20, 0], dtype=torch.int32, device=cuda_device)
+    new = torch.ones(3, 2, 64, dtype=torch.bfloat16, device=cuda_device)
+    for extra in ({}, dict(k_new=new, v_new=new)):
+        status.zero_()
+        out, lse = decode_attention(q, none, none, lens, table, status=status, return_lse=True, **extra)
+        assert int(status) == _abi.XLPK_ERR_INVALID_ARG
+        assert bool(out[1].isnan().all()) and bool((out[[0, 2]] == 0).all()) and bool((lse[[0, 2]] == -math.inf).all())
+
+
 def test_refusals(cuda_device):
     s = make(2, [20, 30], 4, 2, 64, 16)
     q, k, v, lens, table = s["q"], s["k"], s["v"], s["lens"], s["table"]
