@@ -158,6 +158,14 @@ struct Shape {
   static constexpr bool LOW = WIDE && QT > 1;           // the lower terms' scores have sums of their own (else: rows 8-15)
   static constexpr float SHIFT = KV8 ? 10.f : 0.f;      // p is held times 2^SHIFT: fp16 has 2^-14 for its lower term then
   static constexpr int SLOT = ROWS * (D + 2);           // floats of a partial result
+  static constexpr int FOLD = WIDE ? 32 : 64;           // tiles of a warp between additions to its sum in memory
+
+  // Where the 4 dims from 4 c of a head stand in the merge scratch's row: swizzled so that lanes that write at the
+  // same time (all t, and consecutive heads) do so in different banks.
+  __device__ static int place(int head, int c) {
+    if (!KV8) return (c ^ (head & 3) << 1) * 4;
+    return (D == 128 ? c ^ (c >> 3 & 3) ^ (head & 1) << 2 : c ^ (c >> 3 & 1) ^ (head & 1) << 1) * 4;
+  }
 };
 
 __device__ inline void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
@@ -581,192 +589,236 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
         for (int k = 0; k < S::QT; ++k) q[r][k][i] = term<S::KV8>(v[2 * i], v[2 * i + 1]);
     }
 
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool bad = false;
+    int i = w.i + rank;
 
+    // Sums of MMAs are cut off, not rounded, so over many tiles they fall behind (by 2.4e-5 to 5.4e-5 where a
+    // warp sums up 590 to 886 tiles of positive values).  Every FOLD tiles a warp adds them to a sum in its scratch,
+    // which is rounded.
 #pragma unroll 1
-    for (int i = w.i + rank; i < w.end; i += 2 * team) {
-      const bool pair = i + team < w.end;
-      asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
-      __syncwarp();   // V was copied by other lanes too
-      const int stage2 = stage + 1 == S::STAGES ? 0 : stage + 1;
-      // ---- scores: positions are the columns, two tiles side by side, so that four chains of MMAs
-      // run at once.  (Where there is no second tile, what is in its slot is multiplied and masked.)
-      float s[4][4];
+    while (i < w.end) {
+      float o[D / 8][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      float low[S::LOW ? 4 : 1][4] = {};   // what the lower terms add: each sum loses its own last bits only
+      for (int i2 = 0; i2 < D / 8; ++i2) o[i2][0] = o[i2][1] = o[i2][2] = o[i2][3] = 0.f;
+      const int stop = min(w.end, i + S::FOLD * team);
+#pragma unroll 1
+      for (; i < stop; i += 2 * team) {
+        const bool pair = i + team < w.end;
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::STAGES - 2) : "memory");
+        __syncwarp();   // V was copied by other lanes too
+        const int stage2 = stage + 1 == S::STAGES ? 0 : stage + 1;
+        // ---- scores: positions are the columns, two tiles side by side, so that four chains of MMAs
+        // run at once.  (Where there is no second tile, what is in its slot is multiplied and masked.)
+        float s[4][4];
 #pragma unroll
-      for (int n0 = 0; n0 < 4; n0 += S::CHAINS)
+        for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        float low[S::LOW ? 4 : 1][4] = {};   // what the lower terms add: each sum loses its own last bits only
 #pragma unroll
-      for (int j = 0; j < S::KC; ++j) {
-        constexpr int NB = S::KV8 ? 8 : 4;
-        uint32_t kb[S::CHAINS][NB];
+        for (int n0 = 0; n0 < 4; n0 += S::CHAINS)
 #pragma unroll
-        for (int i = 0; i < S::CHAINS; ++i) {
-          const int nt = n0 + i;
-          const uint4 k4 = *reinterpret_cast<const uint4*>(queue_at + (nt >> 1 ? stage2 : stage) * S::STAGE +
-                                                           (((nt & 1) * S::KC + j) * 32 + lane) * 16);
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int j = 0; j < S::KC; ++j) {
+          constexpr int NB = S::KV8 ? 8 : 4;
+          uint32_t kb[S::CHAINS][NB];
 #pragma unroll
-          for (int i2 = 0; i2 < 4; ++i2) {
-            if (S::KV8)
-              kb[i][(2 * i2) % NB] = widen(kw[i2]), kb[i][(2 * i2 + 1) % NB] = widen_high(kw[i2]);
-            else
-              kb[i][i2] = kw[i2];
-          }
-        }
+          for (int i = 0; i < S::CHAINS; ++i) {
+            const int nt = n0 + i;
+            const uint4 k4 = *reinterpret_cast<const uint4*>(queue_at + (nt >> 1 ? stage2 : stage) * S::STAGE +
+                                                             (((nt & 1) * S::KC + j) * 32 + lane) * 16);
+            const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-        for (int p = 0; p < NB; p += 2) {
-          const int c = j * NB + p;
-#pragma unroll
-          for (int k = 0; k < (S::WIDE ? S::QT : (S::QT + 1) / 2); ++k)
-#pragma unroll
-            for (int i = 0; i < S::CHAINS; ++i) {
-              float(&sc)[4] = s[n0 + i];
-              if (S::WIDE)
-                mma(S::LOW && k > 0 ? low[(n0 + i) * S::LOW] : sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[i][p], kb[i][p + 1], S::KV8);
-              else if (2 * k + 1 < S::QT)
-                mma(sc, q[0][2 * k][c], q[0][(2 * k + 1) % S::QT][c], q[0][2 * k][c + 1], q[0][(2 * k + 1) % S::QT][c + 1],
-                    kb[i][p], kb[i][p + 1], S::KV8);
+            for (int i2 = 0; i2 < 4; ++i2) {
+              if (S::KV8)
+                kb[i][(2 * i2) % NB] = widen(kw[i2]), kb[i][(2 * i2 + 1) % NB] = widen_high(kw[i2]);
               else
-                // (a third term joins the second)
-                mma(sc, S::QT > 1 ? 0 : q[0][2 * k][c], S::QT > 1 ? q[0][2 * k][c] : 0, S::QT > 1 ? 0 : q[0][2 * k][c + 1],
-                    S::QT > 1 ? q[0][2 * k][c + 1] : 0, kb[i][p], kb[i][p + 1], S::KV8);
+                kb[i][i2] = kw[i2];
             }
+          }
+#pragma unroll
+          for (int p = 0; p < NB; p += 2) {
+            const int c = j * NB + p;
+#pragma unroll
+            for (int k = 0; k < (S::WIDE ? S::QT : (S::QT + 1) / 2); ++k)
+#pragma unroll
+              for (int i = 0; i < S::CHAINS; ++i) {
+                float(&sc)[4] = s[n0 + i];
+                if (S::WIDE)
+                  mma(S::LOW && k > 0 ? low[(n0 + i) * S::LOW] : sc, q[0][k][c], q[S::WIDE][k][c], q[0][k][c + 1], q[S::WIDE][k][c + 1], kb[i][p], kb[i][p + 1], S::KV8);
+                else if (2 * k + 1 < S::QT)
+                  mma(sc, q[0][2 * k][c], q[0][(2 * k + 1) % S::QT][c], q[0][2 * k][c + 1], q[0][(2 * k + 1) % S::QT][c + 1],
+                      kb[i][p], kb[i][p + 1], S::KV8);
+                else
+                  // (a third term joins the second)
+                  mma(sc, S::QT > 1 ? 0 : q[0][2 * k][c], S::QT > 1 ? q[0][2 * k][c] : 0, S::QT > 1 ? 0 : q[0][2 * k][c + 1],
+                      S::QT > 1 ? q[0][2 * k][c + 1] : 0, kb[i][p], kb[i][p + 1], S::KV8);
+              }
+          }
         }
-      }
-      if (!S::WIDE && S::QT > 1)
+        if (!S::WIDE && S::QT > 1)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
-      if (S::LOW)
+          for (int nt = 0; nt < 4; ++nt) s[nt][0] += s[nt][2], s[nt][1] += s[nt][3];
+        if (S::LOW)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[nt][c] += low[nt * S::LOW][c];
-      // ---- online softmax over the two tiles
+            for (int c = 0; c < 4; ++c) s[nt][c] += low[nt * S::LOW][c];
+        // ---- online softmax over the two tiles
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int pos = tile_pos(w.s, i + half * team);
-        if ((half && !pair) || pos + kTile > w.s.n || (pos < w.s.lo && pos + kTile > a.sinks)) {
+        for (int half = 0; half < 2; ++half) {
+          const int pos = tile_pos(w.s, i + half * team);
+          if ((half && !pair) || pos + kTile > w.s.n || (pos < w.s.lo && pos + kTile > a.sinks)) {
 #pragma unroll
-          for (int n2 = 0; n2 < 2; ++n2)
+            for (int n2 = 0; n2 < 2; ++n2)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if ((half && !pair) || !visible(a, w.s, pos + 8 * n2 + 2 * t + (c & 1))) s[half * 2 + n2][c] = -INFINITY;
+              for (int c = 0; c < 4; ++c)
+                if ((half && !pair) || !visible(a, w.s, pos + 8 * n2 + 2 * t + (c & 1))) s[half * 2 + n2][c] = -INFINITY;
+          }
         }
-      }
-      constexpr int NR = S::WIDE ? 2 : 1;
-      uint32_t pt[NR][S::PT][4];
-      bool grow = false;
-      float fall[2];
+        constexpr int NR = S::WIDE ? 2 : 1;
+        uint32_t pt[NR][S::PT][4];
+        bool grow = false;
+        float fall[2];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        float top = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+        for (int r = 0; r < NR; ++r) {
+          float top = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
 #pragma unroll
-        for (int nt = 1; nt < 4; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        // The running "maximum" is what exponents are measured from: the maximum less SHIFT, rounded, and the
-        // same number for p, for what is rescaled and for the joins, so that its rounding cancels.
-        float mult = S::KV8 ? rs[r] : args.s2;
-        if (fabsf(top * mult) >= kFarScore) {
-          // Out here a rounded maximum is far from the product that it is rounded from (2^27: 8, which fp16
-          // does not stand): scores are rounded first, as coarsely, and the largest has exponent 0.
+          for (int nt = 1; nt < 4; ++nt) top = fmaxf(top, fmaxf(s[nt][2 * r], s[nt][2 * r + 1]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          // The running "maximum" is what exponents are measured from: the maximum less SHIFT, rounded, and the
+          // same number for p, for what is rescaled and for the joins, so that its rounding cancels.
+          float mult = S::KV8 ? rs[r] : args.s2;
+          if (fabsf(top * mult) >= kFarScore) {
+            // Out here a rounded maximum is far from the product that it is rounded from (2^27: 8, which fp16
+            // does not stand): scores are rounded first, as coarsely, and the largest has exponent 0.
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) s[nt][2 * r] *= mult, s[nt][2 * r + 1] *= mult;
-          top = fmaxf(top * mult, m[r]);
-          mult = 1.f;
-        } else {
-          top = fmaxf(fmaf(top, mult, -S::SHIFT), m[r]);
-        }
-        const float base = top == -INFINITY ? 0.f : top;
-        fall[r] = ex2(m[r] - base);
-        grow = grow || top != m[r];
-        m[r] = top;
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          // (the exponent is rounded once, near SHIFT where it counts)
-          float p0 = ex2(fmaf(s[nt][2 * r], mult, -base)), p1 = ex2(fmaf(s[nt][2 * r + 1], mult, -base));
-          sum += p0 + p1;
-#pragma unroll
-          for (int k = 0; k < S::PT; ++k) pt[r][k][nt] = term<S::KV8>(p0, p1);
-        }
-        l[r] = l[r] * fall[r] + sum;
-      }
-      if (__any_sync(~0u, grow)) {
-#pragma unroll
-        for (int i2 = 0; i2 < D / 8; ++i2) {
-          o[i2][0] *= fall[0], o[i2][1] *= fall[0];
-          o[i2][2] *= fall[NR - 1], o[i2][3] *= fall[NR - 1];
-        }
-      }
-      // ---- o += p v
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half && !pair) break;
-        const int lo = half * 2, hi = half * 2 + 1;
-        auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
-          if (S::WIDE) {
-#pragma unroll
-            for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][lo], pt[NR - 1][k][lo], pt[0][k][hi], pt[NR - 1][k][hi], b0, b1, S::KV8);
+            for (int nt = 0; nt < 4; ++nt) s[nt][2 * r] *= mult, s[nt][2 * r + 1] *= mult;
+            top = fmaxf(top * mult, m[r]);
+            mult = 1.f;
           } else {
-            mma(c, pt[0][0][lo], pt[0][1][lo], pt[0][0][hi], pt[0][1][hi], b0, b1, S::KV8);
-            if (S::PT > 2) mma(c, 0, pt[0][S::PT - 1][lo], 0, pt[0][S::PT - 1][hi], b0, b1, S::KV8);
+            top = fmaxf(fmaf(top, mult, -S::SHIFT), m[r]);
           }
-        };
-        const int slot = half ? stage2 : stage;
-        if (!S::KV8) {
-          // lanes 0-7, 8-15: rows 0-7 and 8-15 of one chunk, 16-31: of the next
-          const int row = lane & 15;
-          const uint32_t base = queue + slot * S::STAGE + S::KBYTES + row * D * 2;
+          const float base = top == -INFINITY ? 0.f : top;
+          fall[r] = ex2(m[r] - base);
+          grow = grow || top != m[r];
+          m[r] = top;
+          float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            uint32_t b[4];
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
-                         : "r"(base + (((2 * j + (lane >> 4)) ^ (row & 7)) & (D / 8 - 1)) * 16)
-                         : "memory");
-            pv(o[2 * j], b[0], b[1]);
-            pv(o[2 * j + 1], b[2], b[3]);
+          for (int nt = 0; nt < 4; ++nt) {
+            // (the exponent is rounded once, near SHIFT where it counts)
+            float p0 = ex2(fmaf(s[nt][2 * r], mult, -base)), p1 = ex2(fmaf(s[nt][2 * r + 1], mult, -base));
+            sum += p0 + p1;
+#pragma unroll
+            for (int k = 0; k < S::PT; ++k) pt[r][k][nt] = term<S::KV8>(p0, p1);
           }
-        } else {
-          const uint8_t* at = queue_at + slot * S::STAGE;
-          uint32_t v[4][4];
+          l[r] = l[r] * fall[r] + sum;
+        }
+        if (__any_sync(~0u, grow)) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint8_t* p = at + v_slot(r, 0);
-            if (S::VB == 16) {
-              const uint4 u = *reinterpret_cast<const uint4*>(p);
-              v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+          for (int i2 = 0; i2 < D / 8; ++i2) {
+            o[i2][0] *= fall[0], o[i2][1] *= fall[0];
+            o[i2][2] *= fall[NR - 1], o[i2][3] *= fall[NR - 1];
+          }
+        }
+        // ---- o += p v
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (half && !pair) break;
+          const int lo = half * 2, hi = half * 2 + 1;
+          auto pv = [&](float(&c)[4], uint32_t b0, uint32_t b1) {
+            if (S::WIDE) {
+#pragma unroll
+              for (int k = 0; k < S::PT; ++k) mma(c, pt[0][k][lo], pt[NR - 1][k][lo], pt[0][k][hi], pt[NR - 1][k][hi], b0, b1, S::KV8);
             } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(p);
-              v[r][0] = u.x, v[r][1] = u.y;
+              mma(c, pt[0][0][lo], pt[0][1][lo], pt[0][0][hi], pt[0][1][hi], b0, b1, S::KV8);
+              if (S::PT > 2) mma(c, 0, pt[0][S::PT - 1][lo], 0, pt[0][S::PT - 1][hi], b0, b1, S::KV8);
             }
+          };
+          const int slot = half ? stage2 : stage;
+          if (!S::KV8) {
+            // lanes 0-7, 8-15: rows 0-7 and 8-15 of one chunk, 16-31: of the next
+            const int row = lane & 15;
+            const uint32_t base = queue + slot * S::STAGE + S::KBYTES + row * D * 2;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t b[4];
+              asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                           : "r"(base + (((2 * j + (lane >> 4)) ^ (row & 7)) & (D / 8 - 1)) * 16)
+                           : "memory");
+              pv(o[2 * j], b[0], b[1]);
+              pv(o[2 * j + 1], b[2], b[3]);
+            }
+          } else {
+            const uint8_t* at = queue_at + slot * S::STAGE;
+            uint32_t v[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint8_t* p = at + v_slot(r, 0);
+              if (S::VB == 16) {
+                const uint4 u = *reinterpret_cast<const uint4*>(p);
+                v[r][0] = u.x, v[r][1] = u.y, v[r][2] = u.z, v[r][3] = u.w;
+              } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(p);
+                v[r][0] = u.x, v[r][1] = u.y;
+              }
+            }
+#pragma unroll
+            for (int i2 = 0; i2 < S::VB / 4; ++i2)
+#pragma unroll
+              for (int h2 = 0; h2 < 2; ++h2) {
+                // codes of two positions side by side, two dims in a register
+                const uint32_t e = __byte_perm(v[0][i2], v[1][i2], h2 ? 0x7362 : 0x5140);
+                const uint32_t d = __byte_perm(v[2][i2], v[3][i2], h2 ? 0x7362 : 0x5140);
+                pv(o[i2 * 4 + h2 * 2], widen(e), widen(d));
+                pv(o[i2 * 4 + h2 * 2 + 1], widen_high(e), widen_high(d));
+              }
           }
-#pragma unroll
-          for (int i2 = 0; i2 < S::VB / 4; ++i2)
-#pragma unroll
-            for (int h2 = 0; h2 < 2; ++h2) {
-              // codes of two positions side by side, two dims in a register
-              const uint32_t e = __byte_perm(v[0][i2], v[1][i2], h2 ? 0x7362 : 0x5140);
-              const uint32_t d = __byte_perm(v[2][i2], v[3][i2], h2 ? 0x7362 : 0x5140);
-              pv(o[i2 * 4 + h2 * 2], widen(e), widen(d));
-              pv(o[i2 * 4 + h2 * 2 + 1], widen_high(e), widen_high(d));
-            }
+        }
+        bad = bad || (bad_stages >> stage & 1) || (pair && bad_stages >> stage2 & 1);
+        __syncwarp();   // all lanes have read what is overwritten
+        fetch(stage);
+        stage = stage2;
+        if (pair) {
+          fetch(stage);
+          stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
       }
-      bad = bad || (bad_stages >> stage & 1) || (pair && bad_stages >> stage2 & 1);
-      __syncwarp();   // all lanes have read what is overwritten
-      fetch(stage);
-      stage = stage2;
-      if (pair) {
-        fetch(stage);
-        stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+
+      const bool more_of_it = stop > w.i + rank + S::FOLD * team;   // the scratch holds the sum of earlier tiles
+#pragma unroll
+      for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
+        const int head = g + 8 * r;
+        float* const row = merge + (warp * S::ROWS + head) * D;
+        const float back = more_of_it ? ex2(merge_m[warp * S::ROWS + head] - m[r]) : 0.f;
+        const auto value = [&](int i2, int half, float before) {
+          const float v = S::WIDE ? o[i2][2 * r + half] : o[i2][half] + o[i2][2 + half];
+          return more_of_it ? fmaf(before, back, v) : v;
+        };
+        if (head >= group) continue;
+        if (S::KV8) {   // a lane's accumulators are two runs of D / 8 consecutive dims
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i2 = 0; i2 < D / 8; i2 += 4) {
+              float4* const p = reinterpret_cast<float4*>(row + S::place(head, (2 * t + half) * (D / 32) + i2 / 4));
+              const float4 b = *p;
+              *p = make_float4(value(i2, half, b.x), value(i2 + 1, half, b.y), value(i2 + 2, half, b.z), value(i2 + 3, half, b.w));
+            }
+        } else {
+#pragma unroll
+          for (int i2 = 0; i2 < D / 8; ++i2) {
+            float2* const p = reinterpret_cast<float2*>(row + S::place(head, 2 * i2 + (t >> 1)) + (t & 1) * 2);
+            const float2 b = *p;
+            *p = make_float2(value(i2, 0, b.x), value(i2, 1, b.y));
+          }
+        }
       }
+      __syncwarp();   // all have read the maximum that the sum was measured from
+#pragma unroll
+      for (int r = 0; r < (S::WIDE ? 2 : 1); ++r)
+        if (t == 0) merge_m[warp * S::ROWS + g + 8 * r] = m[r];
+      __syncwarp();
     }
 
     // ---- the warps' results joined
@@ -776,37 +828,7 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
       if (bad) l[r] = __int_as_float(0x7fffffff);
-      if (t == 0 && rank < active) {
-        merge_m[warp * S::ROWS + g + 8 * r] = m[r];
-        merge_l[warp * S::ROWS + g + 8 * r] = l[r];
-      }
-    }
-    worker_sync();
-    if (rank < active) {
-#pragma unroll
-      for (int r = 0; r < (S::WIDE ? 2 : 1); ++r) {
-        const int head = g + 8 * r;
-        if (head >= group) continue;
-        float top = -INFINITY;
-        for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[(lead + k) * S::ROWS + head]);
-        const float e = top == -INFINITY ? 0.f : ex2(m[r] - top);
-        float* row = merge + (warp * S::ROWS + head) * D;
-        const auto value = [&](int i, int half) {
-          const float* acc = o[i];
-          return (S::WIDE ? acc[2 * r + half] : acc[half] + acc[2 + half]) * e;
-        };
-        if (S::KV8) {   // a lane's accumulators are two runs of D / 8 consecutive dims
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int i = 0; i < D / 8; i += 4)
-              *reinterpret_cast<float4*>(row + (2 * t + half) * (D / 8) + i) =
-                  make_float4(value(i, half), value(i + 1, half), value(i + 2, half), value(i + 3, half));
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<float2*>(row + i * 8 + 2 * t) = make_float2(value(i, 0), value(i, 1));
-        }
-      }
+      if (t == 0 && rank < active) merge_l[warp * S::ROWS + g + 8 * r] = l[r];
     }
     worker_sync();
     const bool begins = w.i == 0, ends = w.end == w.s.tiles;
@@ -817,9 +839,10 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
       float top = -INFINITY, den = 0.f;
       for (int k = 0; k < active; ++k) top = fmaxf(top, merge_m[(lead + k) * S::ROWS + head]);
       for (int k = 0; k < active; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(merge + ((lead + k) * S::ROWS + head) * D + d);
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        den += merge_l[(lead + k) * S::ROWS + head] * (top == -INFINITY ? 0.f : ex2(merge_m[(lead + k) * S::ROWS + head] - top));
+        const float4 v = *reinterpret_cast<const float4*>(merge + ((lead + k) * S::ROWS + head) * D + S::place(head, d / 4));
+        const float e = top == -INFINITY ? 0.f : ex2(merge_m[(lead + k) * S::ROWS + head] - top);
+        sum.x += e * v.x, sum.y += e * v.y, sum.z += e * v.z, sum.w += e * v.w;
+        den += e * merge_l[(lead + k) * S::ROWS + head];
       }
       if (begins && ends) {
         const float f = den == 0 ? 0.f : (S::KV8 ? a.v_scale : 1.f) / den;

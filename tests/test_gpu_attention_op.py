@@ -270,6 +270,31 @@ def test_scores_of_any_finite_size(cuda_device, power, H, KH, D, io, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,D", [(4, 64), (4, 128), (16, 64), (12, 128)])
+def test_long_sums_do_not_fall_behind(cuda_device, H, D, kv):
+    """Sums of the tensor cores are cut off, not rounded: less than a step (2^-23) for each product added. Where
+    all values are positive that is a bias, which grows with the positions that one warp sums up: here
+    590 to 886 tiles of 16.
+    Over at most 64 tiles (32, of up to 3 products each, with more than 8 heads) whose sum grows evenly from nothing
+    it is below 64 (96) halves of a step, 2^-24, on average over the outputs; exponentials add 2^-22, the denominator's
+    rounded sums and the rest 2^-22."""
+    B, n = 1024, 16384
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.randn(1, 1, n, D, generator=g, device="cuda")
+    v = 1 + torch.rand(1, 1, n, D, generator=g, device="cuda")
+    k, v = (t.to(E4M3) if kv == "e4m3" else t.to(torch.bfloat16) for t in (k, v))
+    q = torch.randn(B, H, D, generator=g, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    out, _ = decode_attention(q, k.expand(B, -1, -1, -1), v.expand(B, -1, -1, -1), lens, return_lse=True)
+    off = []
+    for part, got in zip(q.split(64), out.split(64)):
+        p = torch.softmax(torch.einsum("bhd,td->bht", part.double(), k[0, 0].double()) / math.sqrt(D), 2)
+        off.append(got.double() / torch.einsum("bht,td->bhd", p, v[0, 0].double()) - 1)
+    bias = float(torch.cat(off).mean())
+    assert abs(bias) <= (64 if H <= 8 else 96) * 2.0 ** -24 + 2.0 ** -21, bias
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
 @pytest.mark.parametrize("size,scale", [(2.0 ** -100, 2.0 ** -100), (2.0 ** -120, 2.0 ** -149), (0.0, 2.0 ** 126), (1.0, 2.0 ** -149)])
 def test_scores_that_vanish(cuda_device, size, scale, H, KH, D, kv):
