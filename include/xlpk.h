@@ -510,9 +510,9 @@ xlpk_status xlpk_decode_attention(const xlpk_attention_args* args, void* workspa
  * [page_size][row_bytes].  Row r of the table is a sequence of seq_lens[r]
  * positions; an entry outside [0, n_pages) holds no page (the calls write -1).
  * refs[p] counts the entries that name page p, plus the references that the
- * caller keeps besides (a prefix held for later); a page with refs 0 is free.  Table, lengths and counts are device
- * memory that the calls update in place, so a loop of them with decode calls
- * needs no host copy.  Fresh pages are always the lowest-numbered free ones, in
+ * caller keeps besides (a prefix held for later); a page with refs 0 is free.
+ * Table, lengths and counts are device memory that the calls update in place, so
+ * a loop of them with decode calls needs no host copy.  Fresh pages are always the lowest-numbered free ones, in
  * row order: results do not depend on timing.
  * A call that cannot be done changes nothing and writes why to *status_dev:
  * XLPK_ERR_OOM (too few free pages), XLPK_ERR_KV_FULL (a row past its table) or
@@ -545,11 +545,16 @@ xlpk_status xlpk_pages_fork(const xlpk_page_pool* pool, const int32_t* parents_d
                             int64_t workspace_bytes, void* stream);
 
 /* Each row gets the pages it lacks to hold positions [seq_lens[r], want[r]).
- * Lengths are not changed. */
+ * Lengths are not changed.  Pages that a row has are taken as they are: a row that
+ * shares one with others is not to be written there (a length set back into a
+ * page with other references; whole pages alone are shared by a fork). */
 xlpk_status xlpk_pages_reserve(const xlpk_page_pool* pool, const int32_t* want_dev, void* stream);
 
 /* Give back the pages that a sliding window has passed: those whose positions
- * are all < seq_lens[r] - window and >= sinks.  window 0: none. */
+ * are all < seq_lens[r] - window and >= sinks.  window 0: none.
+ * For caches that are read through a window, as xlpk_decode_attention does.  A
+ * handle's decode has none: it reads every position, and a page that is gone
+ * from its table makes it report XLPK_ERR_INVALID_ARG. */
 xlpk_status xlpk_pages_trim(const xlpk_page_pool* pool, int32_t window, int32_t sinks, void* stream);
 
 /* Move the live pages (refs > 0) to the numbers below their count: the k-th

@@ -275,8 +275,9 @@ class Engine:
     def page_pool(self, seq_lens, refs=None):
         """The paged cache's ops.PagePool: `seq_lens` int32 CUDA tensor [B] of positions
         in the cache.  Its calls change the table that later decodes read; name the
-        lengths they left to set_state.  (A table or pools that are assigned to it are
-        not the engine's.)"""
+        lengths they left to set_state.  The decode has no window: after a trim it stops at
+        the first page that is gone (trim serves layers that read the cache through
+        decode_attention).  A table or pools that are assigned to it are not the engine's."""
         from .ops import PagePool
         _, k, v, table = self._refs
         if table is None:

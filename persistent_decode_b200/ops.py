@@ -299,11 +299,13 @@ class PagePool:
         self._call("xlpk_pages_fork", stream, row=parents, row_name="parents", workspace=True)
 
     def reserve(self, want, stream=None) -> None:
-        """xlpk_pages_reserve: pages so that row r can hold want[r] positions; `want` int32 [rows]."""
+        """xlpk_pages_reserve: pages so that row r can hold want[r] positions; `want` int32 [rows].
+        Pages that a row shares with others are not copied first."""
         self._call("xlpk_pages_reserve", stream, row=want, row_name="want")
 
     def trim(self, window: int, sinks: int = 0, stream=None) -> None:
-        """xlpk_pages_trim: give back the pages a sliding window has passed."""
+        """xlpk_pages_trim: give back the pages a sliding window has passed (decode_attention's;
+        Engine's decode has none and stops at a page that is gone)."""
         self._call("xlpk_pages_trim", stream, _int32(window, "window"), _int32(sinks, "sinks"))
 
     def compact(self, stream=None):
