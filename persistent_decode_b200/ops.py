@@ -227,15 +227,16 @@ class PagePool:
     """
 
     def __init__(self, k, v, page_table, seq_lens, refs=None, status=None):
-        _tensor(k, "k", 5, _KV, -1)
-        _tensor(page_table, "page_table", 2, _I32, k.get_device())
         if refs is None:
+            _tensor(k, "k", 5, _KV, -1)
+            _tensor(page_table, "page_table", 2, _I32, k.get_device())
             held, n_pages = page_table.reshape(-1), k.shape[1]
             held = held[(held >= 0) & (held < n_pages)]
             refs = torch.bincount(held, minlength=n_pages).to(torch.int32)
         if status is None:
+            _tensor(k, "k", 5, _KV, -1)
             status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._streams = {}     # handle -> stream of the calls so far, for check()
+        self._streams = set()     # handles of the streams of the calls so far, for check()
         self._bind(k, v, page_table, seq_lens, refs, status)
 
     def _bind(self, k, v, page_table, seq_lens, refs, status) -> None:
@@ -243,8 +244,10 @@ class PagePool:
         _tensor(k, "k", 5, _KV, -1)
         dev = k.get_device()
         _tensor(v, "v", 5, (k.dtype,), dev)
-        for t, name, dim in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1), (refs, "refs", 1), (status, "status", 1)):
-            _tensor(t, name, dim, _I32, dev)
+        _tensor(page_table, "page_table", 2, _I32, dev)
+        _tensor(seq_lens, "seq_lens", 1, _I32, dev)
+        _tensor(refs, "refs", 1, _I32, dev)
+        _tensor(status, "status", 1, _I32, dev)
         L, n_pages, KH, P, D = k.shape
         rows, cols = page_table.shape
         if v.shape != k.shape:
@@ -255,7 +258,7 @@ class PagePool:
                 and refs.is_contiguous()):
             _refuse("pool tensors must be contiguous")
         held = (k, v, page_table, seq_lens, refs, status)
-        at = tuple([t.data_ptr() for t in held])
+        at = [t.data_ptr() for t in held]
         try:
             c = _POOL.pack(*at, L, n_pages, KH, P, D * k.element_size(), rows, cols)
         except struct.error as e:
@@ -273,7 +276,7 @@ class PagePool:
 
     def _call(self, name: str, stream, *args, row=None, row_name: str = "", workspace: bool = False) -> None:
         """`row`: the call's first argument, an int32 tensor of one entry a row."""
-        if tuple([t.data_ptr() for t in self._held]) != self._at:   # one was given other memory (t.data = ..., resize_)
+        if [t.data_ptr() for t in self._held] != self._at:   # one was given other memory (t.data = ..., resize_)
             self._bind(*self._held)
         if row_name:
             _tensor(row, row_name, 1, _I32, self._device)
@@ -282,8 +285,7 @@ class PagePool:
             args = (row.data_ptr(), *args)
 
         def launch(handle):
-            if handle not in self._streams:
-                self._streams[handle] = torch.cuda.current_stream(self._device)
+            self._streams.add(handle)
             if workspace:
                 n = _fn("xlpk_pages_workspace")(self._c)
                 ws = _strided((n or 16,), (1,), torch.uint8)
@@ -329,13 +331,13 @@ class PagePool:
         that it was replayed on, which the caller has to wait for.)"""
         with torch.cuda.device(self._device):
             here = torch.cuda.current_stream()
-            for handle in [h for h in self._streams if h != here.cuda_stream]:
-                there = self._streams[handle]
+            for handle in self._streams - {here.cuda_stream}:
+                there = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
                 with torch.cuda.stream(there):
                     recording = torch.cuda.is_current_stream_capturing()   # what it records has not run
                 if not recording:
                     here.wait_stream(there)
-                    del self._streams[handle]
+                    self._streams.discard(handle)
             st = int(self.status[0])
             if st != _abi.XLPK_OK:
                 self.status[:1] = 0

@@ -450,6 +450,12 @@ def test_check_waits_for_every_stream(cuda_device, how):
         assert e.value.status == _abi.XLPK_ERR_OOM
         assert unchanged(p, snap)
         p.check()
+    for _ in range(30):                 # the other way round: from a side stream, a call on the default one
+        torch.mm(busy, busy)
+    p.reserve(want)
+    with torch.cuda.stream(streams[0]):
+        with pytest.raises(XlpkError):
+            p.check()
     # the status is clear for the next call of another stream, which check() waits for as well
     reserve(streams[0], fits)
     p.check()
