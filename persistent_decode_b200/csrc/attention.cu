@@ -11,20 +11,25 @@
 //
 // Bound.  Each K and V entry is read once and meets n_q / n_kv query heads: 4 to
 // 14 flop a byte, far below the tensor cores' ridge, so the floor is the cache's
-// bytes at HBM rate.  One long sequence comes to 91% of the copy rate (131072
-// positions of 8 kv heads of 128, bf16: 91 us for 537 MB).  What keeps shorter
-// ones from it is fixed: about 4 us from launch to the first data and 3.5 us for
-// the join.  e4m3 halves the bytes and not the work: each code is widened to
-// fp16 by a conversion and the loop issues 334 instructions for a tile of 4 KB,
-// so it runs at 71% of that rate (four of 131072, d 128: 234 us for 1.07 GB).
+// bytes at HBM rate.  (Times: of a captured call replayed, on the device; among
+// calls through Python they are 3 to 22 us longer.)  One long sequence comes to
+// 91% of the copy rate (131072 positions of 8 kv heads of 128, bf16: 91 us for
+// 537 MB).  What keeps shorter ones from it is fixed: about 4 us from launch to
+// the first data and 3.5 us for the join.  e4m3 halves the bytes and not the work:
+// each code is widened to fp16 by a conversion, and a tile of 4 KB takes 341
+// instructions.  They are issued in 37% of cycles, with the tensor pipe active in
+// 28%: the loop waits for its own chain of scores, softmax and p v, with two warps
+// a scheduler, and runs at 71% of the copy rate (four of 131072, d 128: 235 us for
+// 1.07 GB).
 //
-// Precision.  m16n8k16 MMAs with fp32 sums.  Cache entries are exact operands
-// (bf16, or e4m3 widened to fp16); q and p are split into as many 16-bit terms as
-// their type needs: one for a bf16 q, three of bf16 or two of fp16 for an fp32
-// q, two (three with fp32 output) for p, so that p's rounding stays far below
-// the output's.  With up to 8 heads a group the second term sits in rows 8-15 of
-// the A operand and costs no MMA.  The scores never leave registers: the C
-// fragment of q.k is the A fragment of p.v.
+// Precision.  m16n8k16 MMAs with fp32 sums, which are added up rounded every FOLD
+// tiles (they cut off).  Cache entries are exact operands (bf16, or e4m3 widened to
+// fp16); q and p are split into as many 16-bit terms as their type needs: one for
+// a bf16 q, three of bf16 or two of fp16 for an fp32 q, two (three with fp32
+// output) for p, so that p's rounding stays far below the output's.  In fp16,
+// weights below 2^-34 of a tile's largest vanish.  With up to 8 heads a group the
+// second term sits in rows 8-15 of the A operand and costs no MMA.  The scores
+// never leave registers: the C fragment of q.k is the A fragment of p.v.
 //
 // Layout.  A K row is multiplied through a permutation of its dims that lets a
 // lane's 16 bytes of it be its B fragments as they are; likewise e4m3 V.  So a
@@ -136,7 +141,7 @@ struct Shape {
   static constexpr bool IO32 = IO32_;
   // Eight warps have registers for four chains of MMAs.  e4m3 rows of 64 leave enough for twelve and
   // two chains (16 sequences of 8192, d 64: 8 warps 53 us, 12 46, 16 48; four of 131072, d 128: 8 warps
-  // 233 us, 12, which spill, 246).
+  // 233 us, 12, which spill, 246; all when this was chosen, 47 and 235 now).
   static constexpr int WARPS = !WIDE && KV8 && D == 64 ? 12 : 8, THREADS = WARPS * 32;
   static constexpr int CHAINS = WARPS == 8 ? 4 : 2;   // scores' chains of MMAs that run at once
   static constexpr int E = KV8 ? 1 : 2;

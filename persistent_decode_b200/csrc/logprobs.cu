@@ -17,10 +17,12 @@
 // pass it for k = 20, 90 for 64.  They are found again where a thread's marks say
 // so, and ranked by counting.
 //
-// Bound: 1024 rows of 128256 fp32 logits take 94 us, 86% of the copy rate (109
-// with 20 alternatives); rows of bf16 by the instructions for each logit (15 of
-// them at 64007: 333 rows take 20 us, 29 with 64 alternatives, of which 6.6 are
-// memory); single rows by latency (32000: 4.4 us, 6.8 with 5 alternatives).
+// Bound (times of a captured call replayed, on the device; among calls through
+// Python they are 2 to 10 us longer): 1024 rows of 128256 fp32 logits take 96 us, 85%
+// of the copy rate (109 with 20 alternatives); rows of bf16 by the instructions for
+// each logit and the uneven rows of each SM (333 rows of 64007 take 20 us, 29 with 64
+// alternatives, of which 6.6 are memory; no pipe is saturated); single rows by latency
+// (32000: 4.4 us, 7.2 with 5 alternatives).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

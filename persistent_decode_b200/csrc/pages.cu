@@ -7,7 +7,7 @@
 // `refs` as they were, so fresh pages never depend on the order in which counts
 // change.
 //
-// Bound: small calls by the two launches (8 rows forked: 3.9 us on the device),
+// Bound (times on the device): small calls by the two launches (8 rows forked: 3.9 us),
 // large ones by the bytes copied, each read and written once.  Copies use plain
 // 16-byte loads, four in flight a thread and eight CTAs an SM: compacting 54 pages of
 // 8.4 MB takes 165 us, of which the bytes are 140 at copy rate; 31 copies of a
