@@ -327,8 +327,8 @@ class PagePool:
 
     def check(self) -> None:
         """Waits for the calls so far, on whatever streams they were made; raises what stopped one
-        of them, and lets the pool go on.  (Replays of a captured graph are calls of the stream
-        that it was replayed on, which the caller has to wait for.)"""
+        of them, and lets the pool go on.  (The streams have to exist still.  Replays of a captured
+        graph are calls of the stream that it was replayed on, which the caller has to wait for.)"""
         with torch.cuda.device(self._device):
             here = torch.cuda.current_stream()
             for handle in self._streams - {here.cuda_stream}:

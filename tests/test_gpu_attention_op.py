@@ -295,6 +295,37 @@ def test_long_sums_do_not_fall_behind(cuda_device, H, D, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("trend", [20.0, -20.0, 0.0])
+@pytest.mark.parametrize("B,H,KH,D,n", [(1024, 4, 1, 64, 16384), (400, 12, 1, 128, 16384), (2, 16, 8, 64, 262144), (2, 16, 8, 128, 200003),
+                                       (2, 32, 2, 128, 400001)])
+def test_long_sums_whose_maximum_moves(cuda_device, B, H, KH, D, n, trend, kv):
+    # scores that rise or fall by 20 along the sequence, so that what a warp has added up is rescaled again and
+    # again; warps as workers (many sequences), and CTAs (two)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = torch.randn(1, 1, n, D, generator=g, device="cuda") * 0.5
+    k[..., 0] = torch.linspace(0, trend / 2, n, device="cuda")
+    v = torch.randn(1, 1, n, D, generator=g, device="cuda") + 1
+    k, v = (t.to(E4M3) if kv == "e4m3" else t.to(torch.bfloat16) for t in (k, v))
+    q = torch.randn(B, H, D, generator=g, device="cuda")
+    q[..., 0] = 2
+    lens = torch.randint(n // 2, n + 1, (B,), generator=g, device="cuda").int()
+    lens[0] = n
+    out, lse = decode_attention(q, k.expand(B, KH, -1, -1), v.expand(B, KH, -1, -1), lens, scale=1.0, return_lse=True)
+    kk, vv = k[0, 0].double(), v[0, 0].double()
+    for b in range(0, B, max(1, B // 16)):
+        m = int(lens[b])
+        sc = q[b].double() @ kk[:m].T
+        S = (q[b].double().abs() @ kk[:m].abs().T).amax(1)
+        want_lse = torch.logsumexp(sc, 1)
+        p = torch.exp(sc - want_lse[:, None])
+        want, Am = p @ vv[:m], p @ vv[:m].abs()
+        # (a warp's or a CTA's sum of 64 tiles at a time, and these, each added to 2^-23: below T / 16 times that)
+        rel = 2.0 ** -16 * S + m * 2.0 ** -26 + 2.0 ** -15
+        assert bool(((out[b].double() - want).abs() <= Am * rel[:, None] + 2.0 ** -24 * want.abs()).all())
+        assert bool(((lse[b].double() - want_lse).abs() <= rel + 2.0 ** -24 * want_lse.abs()).all())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("H,KH,D", [(8, 2, 64), (16, 1, 128)])
 @pytest.mark.parametrize("size,scale", [(2.0 ** -100, 2.0 ** -100), (2.0 ** -120, 2.0 ** -149), (0.0, 2.0 ** 126), (1.0, 2.0 ** -149)])
 def test_scores_that_vanish(cuda_device, size, scale, H, KH, D, kv):
