@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(S::THREADS, 1) attention_kernel(const __grid_c
       }
       if (S::KV8) {
         // fp16 terms: the row is scaled by the power of two that brings its largest entry to
-        // [2^10, 2^11), where 11 bits of it, and what they leave, are held far below 2^-24 of it.
+        // [2^10, 2^11): 11 bits of each entry and 11 of what they leave hold it to 2^-24 of itself, or to
+        // 2^-35 of the largest.
         // (2^e alone may be out of range, and so may the scale's product with 2^-e before it is whole.)
         float top = 0.f;
 #pragma unroll
